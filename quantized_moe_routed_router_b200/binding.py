@@ -48,6 +48,43 @@ class Info(C.Structure):
                 ("sm_count", C.c_int32), ("launch_tokens", C.c_int32)]
 
 
+class RmsnormArgs(C.Structure):
+    _fields_ = [("rows", C.c_int32), ("hidden", C.c_int32), ("resid_type", C.c_int32), ("delta_type", C.c_int32),
+                ("gamma_type", C.c_int32), ("y_type", C.c_int32), ("eps", C.c_float),
+                ("resid", C.c_void_p), ("ld_resid", C.c_int64), ("delta", C.c_void_p), ("ld_delta", C.c_int64),
+                ("gamma", C.c_void_p), ("resid_out", C.c_void_p), ("ld_resid_out", C.c_int64),
+                ("y", C.c_void_p), ("ld_y", C.c_int64), ("q", C.c_void_p), ("ld_q", C.c_int64),
+                ("q_scale", C.c_void_p), ("qs_row", C.c_int64), ("qs_group", C.c_int64)]
+
+
+class ActQuantArgs(C.Structure):
+    _fields_ = [("rows", C.c_int32), ("inter", C.c_int32), ("act", C.c_int32), ("in_type", C.c_int32),
+                ("act_alpha", C.c_float), ("act_limit", C.c_float),
+                ("gate", C.c_void_p), ("ld_gate", C.c_int64), ("up", C.c_void_p), ("ld_up", C.c_int64),
+                ("q", C.c_void_p), ("ld_q", C.c_int64), ("q_scale", C.c_void_p), ("qs_row", C.c_int64),
+                ("qs_group", C.c_int64)]
+
+
+class Fp8MatmulArgs(C.Structure):
+    _fields_ = [("rows", C.c_int32), ("n", C.c_int32), ("k", C.c_int32), ("num_groups", C.c_int32),
+                ("out_type", C.c_int32), ("reserved", C.c_int32),
+                ("a", C.c_void_p), ("ld_a", C.c_int64), ("a_scale", C.c_void_p), ("as_row", C.c_int64),
+                ("as_block", C.c_int64),
+                ("b", C.c_void_p), ("ld_b", C.c_int64), ("b_group", C.c_int64), ("b_scale", C.c_void_p),
+                ("bs_group", C.c_int64), ("bs_row", C.c_int64), ("bs_block", C.c_int64),
+                ("offsets", C.c_void_p), ("add", C.c_void_p), ("ld_add", C.c_int64),
+                ("out", C.c_void_p), ("ld_out", C.c_int64)]
+
+
+class BalanceArgs(C.Structure):
+    _fields_ = [("rows", C.c_int32), ("experts", C.c_int32), ("top_k", C.c_int32), ("score", C.c_int32),
+                ("dtype", C.c_int32), ("coef", C.c_float),
+                ("logits", C.c_void_p), ("ld_logits", C.c_int64), ("idx", C.c_void_p), ("ld_idx", C.c_int64),
+                ("mask", C.c_void_p), ("dloss", C.c_void_p), ("loss", C.c_void_p), ("prob", C.c_void_p),
+                ("counts", C.c_void_p), ("offsets", C.c_void_p), ("dlogits", C.c_void_p), ("ld_dlogits", C.c_int64),
+                ("workspace", C.c_void_p), ("workspace_bytes", C.c_uint64)]
+
+
 def _load():
     if not os.path.exists(LIB_PATH):
         raise ImportError(f"{LIB_PATH} is not built; run quantized_moe_routed_router_b200.build.build()")
@@ -75,9 +112,16 @@ def _load():
     lib.ts_moe_debug_validate.argtypes = [C.POINTER(Config), C.POINTER(LayerWeights)]
     lib.ts_moe_route_noalloc.argtypes = [vp, vp, vp, i32, i32, i32, i32, i32, vp, i32, vp, vp, vp, vp]
     lib.ts_moe_debug_skew_barrier.argtypes = [vp, vp]
+    lib.ts_moe_rmsnorm.argtypes = [C.POINTER(RmsnormArgs), vp]
+    lib.ts_moe_act_quant.argtypes = [C.POINTER(ActQuantArgs), vp]
+    lib.ts_moe_fp8_matmul.argtypes = [C.POINTER(Fp8MatmulArgs), vp]
+    lib.ts_moe_balance.argtypes = [C.POINTER(BalanceArgs), vp]
+    lib.ts_moe_balance_workspace.argtypes = [C.c_int32, C.c_int32]
+    lib.ts_moe_balance_workspace.restype = C.c_uint64
     for f in ("ts_moe_open", "ts_moe_route", "ts_moe_forward", "ts_moe_device_status", "ts_moe_get_info",
               "ts_moe_set_timing_events", "ts_moe_close", "ts_moe_debug_validate", "ts_moe_route_noalloc",
-              "ts_moe_debug_skew_barrier"):
+              "ts_moe_debug_skew_barrier", "ts_moe_rmsnorm", "ts_moe_act_quant", "ts_moe_fp8_matmul",
+              "ts_moe_balance"):
         getattr(lib, f).restype = C.c_int
     return lib
 
@@ -204,6 +248,206 @@ def route_noalloc(router: torch.Tensor, bias: Optional[torch.Tensor], pes: Optio
                                   _ptr(x), M, _ptr(idx), _ptr(w), _ptr(logits), _stream(stream))
     if st != 0:
         raise TsMoeError(st, lib.ts_moe_last_error(None).decode())
+
+
+# ----------------------------------------------------------------------------- the operators next to the routed half
+
+_DT = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
+
+
+def _refuse(msg: str):
+    raise TsMoeError(1, msg)
+
+
+def _check_op(st: int):
+    if st != 0:
+        raise TsMoeError(st, lib.ts_moe_last_error(None).decode())
+
+
+def _rows(t: torch.Tensor, what: str, rows: int, cols: int, dev: torch.device) -> int:
+    """The row stride of a [rows][cols] tensor on `dev` with a contiguous last dimension."""
+    if t.device != dev:
+        _refuse(f"{what} is on {t.device}, not on {dev}")
+    if t.shape != (rows, cols):
+        _refuse(f"{what} has shape {tuple(t.shape)}, not {(rows, cols)}")
+    ld, inner = t.stride()
+    if inner != 1 and cols > 1:
+        _refuse(f"{what} needs a contiguous last dimension")
+    return ld if rows > 1 and ld >= cols else max(ld, cols) if rows <= 1 else ld
+
+
+def _type(t: torch.Tensor, what: str) -> int:
+    dt = _DT.get(t.dtype)
+    if dt is None:
+        _refuse(f"{what} is {t.dtype}; bfloat16, float16 or float32 is needed")
+    return dt
+
+
+def _flat(t: torch.Tensor, what: str, n: int, dtype, dev: torch.device) -> int:
+    if t.device != dev or t.dtype != dtype or t.numel() != n or not t.is_contiguous():
+        _refuse(f"{what} must be a contiguous {dtype} tensor of {n} elements on {dev}")
+    return t.data_ptr()
+
+
+def _codes(t: torch.Tensor, what: str):
+    if t.dtype != torch.float8_e4m3fn and t.dtype != torch.uint8:
+        _refuse(f"{what} is {t.dtype}; float8_e4m3fn (or its bytes as uint8) is needed")
+
+
+def _scales(t: torch.Tensor, what: str, shape: tuple, dev: torch.device) -> tuple:
+    if t.device != dev or t.dtype != torch.float32 or t.shape != shape:
+        _refuse(f"{what} must be a float32 tensor of shape {shape} on {dev}")
+    return t.stride()
+
+
+def _call(fn, args, dev: torch.device, stream):
+    """Calls on the tensors' own device and, without a stream, on that device's current stream."""
+    if dev.type != "cuda":
+        _refuse("the tensors must be on a CUDA device")
+    if stream is None:
+        stream = torch.cuda.current_stream(dev)
+    if isinstance(stream, torch.cuda.Stream):
+        if stream.device != dev:
+            _refuse(f"the stream belongs to {stream.device}, the tensors to {dev}")
+        stream = stream.cuda_stream
+    if torch.cuda.current_device() == dev.index:
+        _check_op(fn(C.byref(args), stream))
+    else:
+        with torch.cuda.device(dev):
+            _check_op(fn(C.byref(args), stream))
+
+
+def rmsnorm(resid: torch.Tensor, gamma: Optional[torch.Tensor], eps: float, delta: Optional[torch.Tensor] = None,
+            resid_out: Optional[torch.Tensor] = None, y: Optional[torch.Tensor] = None,
+            q: Optional[torch.Tensor] = None, q_scale: Optional[torch.Tensor] = None, stream=None):
+    """ts_moe_rmsnorm: r = resid + delta (kept in resid_out, which may be resid),
+    v = r / sqrt(mean(r^2) + eps) * gamma, written to y [M, H] and/or as 8-bit
+    rows to q [M, H] with q_scale [M, ceil(H / 128)] (any strides)."""
+    M, H = resid.shape
+    dev = resid.device
+    a = RmsnormArgs()
+    a.rows, a.hidden, a.eps = M, H, eps
+    a.resid, a.ld_resid, a.resid_type = resid.data_ptr(), _rows(resid, "resid", M, H, dev), _type(resid, "resid")
+    if delta is not None:
+        a.delta, a.ld_delta, a.delta_type = delta.data_ptr(), _rows(delta, "delta", M, H, dev), _type(delta, "delta")
+    if gamma is not None:
+        a.gamma, a.gamma_type = _flat(gamma, "gamma", H, gamma.dtype, dev), _type(gamma, "gamma")
+    if resid_out is not None:
+        if resid_out.dtype != resid.dtype:
+            _refuse("resid_out must have resid's type")
+        a.resid_out, a.ld_resid_out = resid_out.data_ptr(), _rows(resid_out, "resid_out", M, H, dev)
+    if y is not None:
+        a.y, a.ld_y, a.y_type = y.data_ptr(), _rows(y, "y", M, H, dev), _type(y, "y")
+    if q is not None:
+        _codes(q, "q")
+        a.q, a.ld_q = q.data_ptr(), _rows(q, "q", M, H, dev)
+    if q_scale is not None:
+        a.qs_row, a.qs_group = _scales(q_scale, "q_scale", (M, -(-H // 128)), dev)
+        a.q_scale = q_scale.data_ptr()
+    if M == 0:
+        return
+    _call(lib.ts_moe_rmsnorm, a, dev, stream)
+
+
+def act_quant(gate: torch.Tensor, up: torch.Tensor, act: int, q: torch.Tensor, q_scale: torch.Tensor,
+              act_alpha: float = 1.702, act_limit: float = 7.0, stream=None):
+    """ts_moe_act_quant: the activation of gate and up ([M, I], e.g. two halves
+    of one product) as 8-bit rows q [M, I] with q_scale [M, ceil(I / 128)]."""
+    M, inter = gate.shape
+    dev = gate.device
+    if up.dtype != gate.dtype:
+        _refuse("gate and up must have one type")
+    _codes(q, "q")
+    qs = _scales(q_scale, "q_scale", (M, -(-inter // 128)), dev)
+    a = ActQuantArgs(M, inter, act, _type(gate, "gate"), act_alpha, act_limit,
+                     gate.data_ptr(), _rows(gate, "gate", M, inter, dev), up.data_ptr(), _rows(up, "up", M, inter, dev),
+                     q.data_ptr(), _rows(q, "q", M, inter, dev), q_scale.data_ptr(), qs[0], qs[1])
+    if M == 0:
+        return
+    _call(lib.ts_moe_act_quant, a, dev, stream)
+
+
+def fp8_matmul(a: torch.Tensor, a_scale: torch.Tensor, b: torch.Tensor, b_scale: torch.Tensor, out: torch.Tensor,
+               add: Optional[torch.Tensor] = None, offsets: Optional[torch.Tensor] = None, stream=None):
+    """ts_moe_fp8_matmul: out [M, N] = a [M, K] b^T with scales per row and 128
+    columns (a_scale [M, ceil(K / 128)]) and per 128 x 128 block (b_scale
+    [ceil(N / 128), ceil(K / 128)]), plus add [M, N] in out's type (out itself
+    is allowed).  b is [N, K], or with offsets (int32 [G + 1] on the device)
+    [G, N, K] with b_scale [G, ..., ...]: rows offsets[g] .. offsets[g + 1] - 1
+    use b[g], other rows of out are left as they were."""
+    M, K = a.shape
+    N = out.shape[1]
+    dev = a.device
+    kb = -(-K // 128)
+    _codes(a, "a")
+    _codes(b, "b")
+    sa = _scales(a_scale, "a_scale", (M, kb), dev)
+    if offsets is None:
+        G, group, ldb, off = 1, 0, _rows(b, "b", N, K, dev), None
+        sb = (0,) + tuple(_scales(b_scale, "b_scale", (-(-N // 128), kb), dev))
+    else:
+        if b.dim() != 3:
+            _refuse("b must be [G, N, K] when offsets are given")
+        G, group, ldb = b.shape[0], b.stride(0), _rows(b[0], "b[g]", N, K, dev)
+        sb = _scales(b_scale, "b_scale", (G, -(-N // 128), kb), dev)
+        off = _flat(offsets, "offsets", G + 1, torch.int32, dev)
+    p = Fp8MatmulArgs(M, N, K, G, _type(out, "out"), 0, a.data_ptr(), _rows(a, "a", M, K, dev), a_scale.data_ptr(), sa[0], sa[1],
+                      b.data_ptr(), ldb, group, b_scale.data_ptr(), sb[0], sb[1], sb[2], off)
+    p.out, p.ld_out = out.data_ptr(), _rows(out, "out", M, N, dev)
+    if add is not None:
+        if add.dtype != out.dtype:
+            _refuse("add must have out's type")
+        p.add, p.ld_add = add.data_ptr(), _rows(add, "add", M, N, dev)
+    if M == 0:
+        return
+    _call(lib.ts_moe_fp8_matmul, p, dev, stream)
+
+
+def balance(logits: torch.Tensor, idx: torch.Tensor, score: int, loss: torch.Tensor, counts: torch.Tensor,
+            prob: Optional[torch.Tensor] = None, mask: Optional[torch.Tensor] = None,
+            dlogits: Optional[torch.Tensor] = None, dloss: Optional[torch.Tensor] = None, coef: float = 1.0,
+            offsets: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None, stream=None):
+    """ts_moe_balance: per-expert counts (int32 [E]) and their running sum
+    (offsets, int32 [E + 1]), the mean probabilities prob (float32 [E]), the
+    balance loss (float32, one element) and, with dlogits [M, E], its gradient
+    times dloss (float32, one element; None = 1).  mask: bool or uint8 [M], rows
+    that count.  Without a workspace one is taken from torch's allocator."""
+    M, E = logits.shape
+    dev = logits.device
+    K = idx.shape[-1]
+    if idx.dtype != torch.int32:
+        _refuse(f"idx is {idx.dtype}; int32 is needed")
+    a = BalanceArgs(M, E, K, score, _type(logits, "logits"), coef, logits.data_ptr(), _rows(logits, "logits", M, E, dev),
+                    idx.data_ptr(), _rows(idx, "idx", M, K, dev))
+    if mask is not None:
+        if mask.dtype not in (torch.bool, torch.uint8):
+            _refuse(f"mask is {mask.dtype}; bool or uint8 is needed")
+        a.mask = _flat(mask, "mask", M, mask.dtype, dev)
+    if dloss is not None:
+        a.dloss = _flat(dloss, "dloss", 1, torch.float32, dev)
+    a.loss = _flat(loss, "loss", 1, torch.float32, dev)
+    a.counts = _flat(counts, "counts", E, torch.int32, dev)
+    if prob is not None:
+        a.prob = _flat(prob, "prob", E, torch.float32, dev)
+    if offsets is not None:
+        a.offsets = _flat(offsets, "offsets", E + 1, torch.int32, dev)
+    if dlogits is not None:
+        if dlogits.dtype != logits.dtype:
+            _refuse("dlogits must have the type of logits")
+        a.dlogits, a.ld_dlogits = dlogits.data_ptr(), _rows(dlogits, "dlogits", M, E, dev)
+    need = lib.ts_moe_balance_workspace(M, E)
+    if workspace is None:
+        s = stream if isinstance(stream, torch.cuda.Stream) else None
+        if stream is not None and s is None:
+            _refuse("a raw stream handle needs a workspace of the caller's")
+        if dev.type != "cuda":
+            _refuse("the tensors must be on a CUDA device")
+        with torch.cuda.stream(s):   # None: the current stream
+            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    elif workspace.device != dev or not workspace.is_contiguous():
+        _refuse(f"workspace must be a contiguous tensor on {dev}")
+    a.workspace, a.workspace_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    _call(lib.ts_moe_balance, a, dev, stream)
 
 
 def validate(shape: "synth.MoEShape", layers: Sequence["synth.LayerBlobs"], **cfg_over) -> tuple:

@@ -1,0 +1,166 @@
+// Element access shared by the operators: eight consecutive elements of a
+// 16- or 32-bit row as float32, and groups of 128 columns as E4M3.
+#pragma once
+#include <cuda_fp8.h>
+
+#include "../../../include/ts_moe_ops.h"
+#include "../common.cuh"
+
+namespace tsm {
+
+constexpr int SCALE_BLOCK = TS_MOE_SCALE_BLOCK;
+constexpr float E4M3_MAX = 448.f;
+constexpr float AMAX_FLOOR = 0x1p-100f;  // the smallest amax a scale is formed from: scale and 1 / scale stay normal
+
+__host__ __device__ inline int cdiv(int a, int b) { return (a + b - 1) / b; }
+__host__ __device__ inline int dt_size(int type) { return type == TS_DT_FP32 ? 4 : 2; }
+
+// Eight elements as they lie in memory: 16-bit types fill `a` only.
+struct Raw8 {
+  uint4 a, b;
+};
+
+// Loads elements [off, off + n) of a row, n <= 8.  VEC: n = 8 and the address
+// is 16-byte aligned; otherwise element by element, the rest zero.
+template <bool VEC>
+TSM_DEV Raw8 load_raw8(const void* base, int type, int64_t off, int n) {
+  Raw8 r;
+  if (VEC) {
+    if (type == TS_DT_FP32) {
+      const uint4* p = (const uint4*)((const float*)base + off);
+      r.a = p[0];
+      r.b = p[1];
+    } else {
+      r.a = *(const uint4*)((const uint16_t*)base + off);
+    }
+    return r;
+  }
+  uint32_t w[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+  if (type == TS_DT_FP32) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (j < n) w[j] = ((const uint32_t*)base)[off + j];
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (j < n) w[j / 2] |= (uint32_t)((const uint16_t*)base)[off + j] << (16 * (j % 2));
+  }
+  r.a = make_uint4(w[0], w[1], w[2], w[3]);
+  r.b = make_uint4(w[4], w[5], w[6], w[7]);
+  return r;
+}
+
+TSM_DEV void cvt8(const Raw8& r, int type, float (&v)[8]) {
+  const uint32_t w[4] = {r.a.x, r.a.y, r.a.z, r.a.w};
+  if (type == TS_DT_BF16) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      v[2 * j] = __uint_as_float(w[j] << 16);
+      v[2 * j + 1] = __uint_as_float(w[j] & 0xFFFF0000u);
+    }
+  } else if (type == TS_DT_FP16) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[j]));
+      v[2 * j] = f.x;
+      v[2 * j + 1] = f.y;
+    }
+  } else {
+    const uint32_t u[4] = {r.b.x, r.b.y, r.b.z, r.b.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      v[j] = __uint_as_float(w[j]);
+      v[4 + j] = __uint_as_float(u[j]);
+    }
+  }
+}
+
+TSM_DEV uint32_t pack2(float x, float y, int type) {
+  if (type == TS_DT_BF16) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
+    return *reinterpret_cast<const uint32_t*>(&h);
+  }
+  const __half2 h = __floats2half2_rn(x, y);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// Eight float32 values rounded once to the type.
+TSM_DEV Raw8 round8(const float (&v)[8], int type) {
+  Raw8 r;
+  if (type == TS_DT_FP32) {
+    r.a = make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]));
+    r.b = make_uint4(__float_as_uint(v[4]), __float_as_uint(v[5]), __float_as_uint(v[6]), __float_as_uint(v[7]));
+  } else {
+    r.a = make_uint4(pack2(v[0], v[1], type), pack2(v[2], v[3], type), pack2(v[4], v[5], type), pack2(v[6], v[7], type));
+    r.b = make_uint4(0, 0, 0, 0);
+  }
+  return r;
+}
+
+template <bool VEC>
+TSM_DEV void store_raw8(void* base, int type, int64_t off, int n, const Raw8& r) {
+  if (VEC) {
+    if (type == TS_DT_FP32) {
+      uint4* p = (uint4*)((float*)base + off);
+      p[0] = r.a;
+      p[1] = r.b;
+    } else {
+      *(uint4*)((uint16_t*)base + off) = r.a;
+    }
+    return;
+  }
+  const uint32_t w[8] = {r.a.x, r.a.y, r.a.z, r.a.w, r.b.x, r.b.y, r.b.z, r.b.w};
+  if (type == TS_DT_FP32) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (j < n) ((uint32_t*)base)[off + j] = w[j];
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (j < n) ((uint16_t*)base)[off + j] = (uint16_t)(w[j / 2] >> (16 * (j % 2)));
+  }
+}
+
+// Maximum that keeps a NaN (fmaxf drops it).
+TSM_DEV float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+
+// Sixteen neighbouring lanes hold the 128 columns of one group, eight each
+// (lanes past the row's end hold zeros).  Writes the group's E4M3 codes and,
+// from its first lane, its scale.  amax / 448 and its reciprocal are formed by
+// IEEE divisions; v * (1 / scale) differs from v / scale by under 2^-23
+// relative, which moves a code only where v / scale lies that close to the
+// middle between two codes.  The conversion saturates, so the group's largest
+// value lands on 448 whichever way that rounds.
+template <bool VEC>
+TSM_DEV void quant_group16(const float (&v)[8], uint8_t* q, int64_t off, int n, float* scale) {
+  float m = 0.f;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) m = max_nan(m, fabsf(v[j]));
+#pragma unroll
+  for (int d = 8; d >= 1; d >>= 1) m = max_nan(m, __shfl_xor_sync(0xFFFFFFFFu, m, d, 16));
+  const float s = max_nan(m, AMAX_FLOOR) / E4M3_MAX;
+  const float inv = 1.f / s;
+  uint32_t w[2];
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(v[4 * j] * inv, v[4 * j + 1] * inv), __NV_SATFINITE, __NV_E4M3);
+    const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(v[4 * j + 2] * inv, v[4 * j + 3] * inv), __NV_SATFINITE, __NV_E4M3);
+    w[j] = lo | hi << 16;
+  }
+  if (n > 0) {
+    if (VEC) {
+      *(uint2*)(q + off) = make_uint2(w[0], w[1]);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (j < n) q[off + j] = (uint8_t)(w[j / 4] >> (8 * (j % 4)));
+    }
+    if ((threadIdx.x & 15) == 0) *scale = s;
+  }
+}
+
+}  // namespace tsm

@@ -15,6 +15,7 @@
 #include "../../include/ts_moe.h"
 #include "../../include/ts_moe_debug.h"
 #include "common.cuh"
+#include "errors.h"
 #include "expert.cuh"
 #include "layout.cuh"
 #include "repack.cuh"
@@ -107,6 +108,19 @@ ts_moe_status fail(ts_moe* h, ts_moe_status st, const std::string& msg) {
 ts_moe_status cuda_fail(ts_moe* h, cudaError_t e, const char* what) {
   return fail(h, TS_MOE_ECUDA, std::string(what) + ": " + cudaGetErrorString(e));
 }
+
+}  // namespace
+
+ts_moe_status tsm::set_last_error(ts_moe_status st, const char* msg) noexcept {
+  try {
+    g_open_error = msg;
+  } catch (...) {
+    g_open_error.clear();
+  }
+  return st;
+}
+
+namespace {
 
 #define TSM_CUDA(h, call)                                     \
   do {                                                        \
