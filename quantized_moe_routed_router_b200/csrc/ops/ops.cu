@@ -5,12 +5,14 @@
 #include <algorithm>
 #include <cmath>
 #include <cstdio>
+#include <cstring>
+#include <mutex>
 
 #include "../../../include/ts_moe_ops.h"
 #include "../errors.h"
 #include "act.cuh"
 #include "balance.cuh"
-#include "matmul_simple.cuh"
+#include "matmul.cuh"
 #include "norm.cuh"
 
 using namespace tsm;
@@ -30,19 +32,140 @@ bool known_type(int t) { return t == TS_DT_BF16 || t == TS_DT_FP16 || t == TS_DT
 bool aligned(const void* p, int64_t ld_bytes, int to) { return (uintptr_t)p % to == 0 && ld_bytes % to == 0; }
 bool aligned_rows(const void* p, int64_t ld, int type) { return !p || aligned(p, ld * dt_size(type), 16); }
 
+// With programmatic dependent launch: the kernel's set-up overlaps the previous kernel's tail, and
+// griddepcontrol.wait orders the data.  cluster: CTAs of a cluster along x.
 template <typename... Params, typename... Args>
-cudaError_t launch(void (*kernel)(Params...), dim3 grid, int block, size_t smem, void* stream, Args... args) {
+cudaError_t launch_clusters(void (*kernel)(Params...), dim3 grid, int block, size_t smem, void* stream, int cluster, const Args&... args) {
   cudaLaunchConfig_t lc = {};
   lc.gridDim = grid;
   lc.blockDim = dim3(block);
   lc.dynamicSmemBytes = smem;
   lc.stream = (cudaStream_t)stream;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = cluster;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   lc.attrs = attr;
-  lc.numAttrs = 1;
+  lc.numAttrs = cluster > 1 ? 2 : 1;
   return cudaLaunchKernelEx(&lc, kernel, args...);
+}
+
+template <typename... Params, typename... Args>
+cudaError_t launch(void (*kernel)(Params...), dim3 grid, int block, size_t smem, void* stream, const Args&... args) {
+  return launch_clusters(kernel, grid, block, smem, stream, 1, args...);
+}
+
+// ----------------------------------------------------------------------------- product
+using EncodeTiled = decltype(&cuTensorMapEncodeTiled);
+constexpr int MAX_DEVICES = 64;
+
+struct MatmulDevice {
+  bool ready = false;
+  int sms = 0;
+};
+std::mutex g_matmul_mu;
+MatmulDevice g_matmul[MAX_DEVICES];
+EncodeTiled g_encode = nullptr;
+
+template <int BT>
+constexpr size_t stream_smem() {
+  return sizeof(StreamSmem<BT>) + 1024;  // the struct starts at a 1024-byte boundary inside
+}
+constexpr size_t tile_smem() { return sizeof(TileSmem) + 1024; }
+
+template <int BT>
+cudaError_t allow_stream() {
+  return cudaFuncSetAttribute(fp8_stream_kernel<BT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)stream_smem<BT>());
+}
+
+// Once per device, with that device current: the SM count, the kernels' shared-memory attributes, and the driver's
+// tensor-map encoder.
+ts_moe_status matmul_setup(const MatmulDevice** out) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return cuda_bad(e, "cudaGetDevice");
+  if (dev < 0 || dev >= MAX_DEVICES) return set_last_error(TS_MOE_EUNSUPPORTED, "device ordinal >= 64");
+  std::lock_guard<std::mutex> lk(g_matmul_mu);
+  MatmulDevice& d = g_matmul[dev];
+  if (!d.ready) {
+    e = cudaDeviceGetAttribute(&d.sms, cudaDevAttrMultiProcessorCount, dev);
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(fp8_tile_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)tile_smem());
+    if (e == cudaSuccess) e = allow_stream<16>();
+    if (e == cudaSuccess) e = allow_stream<32>();
+    if (e == cudaSuccess) e = allow_stream<64>();
+    if (e == cudaSuccess) e = allow_stream<128>();
+    if (e != cudaSuccess) return cuda_bad(e, "fp8_matmul set-up");
+    if (!g_encode) {
+      void* fn = nullptr;
+      cudaDriverEntryPointQueryResult r;
+      e = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &r);
+      if (e != cudaSuccess || r != cudaDriverEntryPointSuccess || !fn)
+        return set_last_error(TS_MOE_ECUDA, "the driver has no cuTensorMapEncodeTiled");
+      g_encode = (EncodeTiled)fn;
+    }
+    d.ready = true;
+  }
+  *out = &d;
+  return TS_MOE_OK;
+}
+
+// Map of 8-bit rows, boxes of box_rows x 128 codes in the 128-byte swizzle; what lies past an extent reads as zero.
+// groups < 0: two dimensions.
+bool encode_rows(CUtensorMap* m, const uint8_t* p, int k, int rows, int64_t ld, int groups, int64_t group, int box_rows) {
+  cuuint64_t dims[3] = {(cuuint64_t)k, (cuuint64_t)rows, (cuuint64_t)std::max(groups, 1)};
+  cuuint64_t strides[2] = {(cuuint64_t)ld, (cuuint64_t)group};
+  cuuint32_t box[3] = {SCALE_BLOCK, (cuuint32_t)box_rows, 1}, one[3] = {1, 1, 1};
+  return g_encode(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, groups < 0 ? 2 : 3, (void*)p, dims, strides, box, one,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int BT>
+cudaError_t launch_stream(const MatmulParams& p, const CUtensorMap& ma, const CUtensorMap& mb, int clusters, void* stream) {
+  return launch_clusters(fp8_stream_kernel<BT>, dim3(clusters * p.splits), ST_THREADS, stream_smem<BT>(), stream, p.splits, p, ma, mb);
+}
+
+// Which kernel, and how its work is cut.
+struct MatmulPlan {
+  int bt;      // rows of an fp8_stream_kernel tile; 0: fp8_tile_kernel
+  int splits;  // CTAs that share K
+  int grid;    // CTAs (tile kernel) or clusters
+  int box_a, box_b;
+};
+
+MatmulPlan matmul_plan(const ts_moe_fp8_matmul_args& a, int sms) {
+  const int kb = cdiv(a.k, SCALE_BLOCK), G = a.num_groups;
+  const int64_t reached = std::min(G, a.rows);            // groups that can hold a row
+  const int64_t mean = cdiv(a.rows, (int)reached);
+  const int64_t tiles = (cdiv(a.rows, TL_M) + reached - 1) * cdiv(a.n, TL_N);
+  MatmulPlan p;
+  if (mean > 128 && tiles >= sms) {
+    p.bt = 0;
+    p.splits = 1;
+    p.grid = (int)std::min<int64_t>(tiles, sms);
+    p.box_a = TL_M;
+    p.box_b = TL_N;
+    return p;
+  }
+  p.bt = G > 1 ? (mean <= 4 ? 16 : mean <= 12 ? 32 : mean <= 32 ? 64 : 128) : (mean <= 16 ? 16 : mean <= 32 ? 32 : mean <= 64 ? 64 : 128);
+  const int64_t items = (cdiv(a.rows, p.bt) + reached - 1) * cdiv(a.n, ST_N);
+  // the number of CTAs per tile that leaves the busiest SM the fewest blocks of K
+  const int per_sm = p.bt == 128 ? 1 : 2;
+  int64_t best = -1;
+  p.splits = 1;
+  for (int s = 1; s <= std::min(8, kb); ++s) {
+    const int64_t cost = cdiv((int)std::min<int64_t>(items * s, 1 << 30), sms) * (int64_t)cdiv(kb, s);
+    if (best < 0 || cost < best) {
+      best = cost;
+      p.splits = s;
+    }
+  }
+  p.grid = (int)std::min<int64_t>(items, std::max(1, sms * per_sm / p.splits));
+  p.box_a = p.bt;
+  p.box_b = ST_N;
+  return p;
 }
 
 ts_moe_status done(cudaError_t e, const char* what) { return e == cudaSuccess ? TS_MOE_OK : cuda_bad(e, what); }
@@ -116,12 +239,39 @@ ts_moe_status ts_moe_fp8_matmul(const ts_moe_fp8_matmul_args* args, void* stream
   if (a.rows == 0) return TS_MOE_OK;
   if (!a.a || !a.a_scale || !a.b || !a.b_scale || !a.out) return bad("fp8_matmul: a, a_scale, b, b_scale and out must be non-NULL");
   if (a.ld_a < a.k || a.ld_b < a.k || a.ld_out < a.n || (a.add && a.ld_add < a.n)) return bad("fp8_matmul: a row stride is smaller than the row");
-  if (!aligned(a.a, a.ld_a, 16) || !aligned(a.b, a.ld_b, 16) || a.b_group % 16)
+  if (!aligned(a.a, a.rows > 1 ? a.ld_a : 0, 16) || !aligned(a.b, a.n > 1 ? a.ld_b : 0, 16) || (a.num_groups > 1 && a.b_group % 16))
     return bad("fp8_matmul: the rows of a and b must start at 16-byte boundaries");
   if (a.num_groups > 1 && a.b_group < (int64_t)(a.n - 1) * a.ld_b + a.k) return bad("fp8_matmul: b_group is smaller than a matrix");
   if (a.add == a.out && a.ld_add != a.ld_out) return bad("fp8_matmul: add in place needs out's stride");
-  const int row_tiles = std::min(cdiv(a.rows, SM_T), 64);
-  return done(launch(fp8_matmul_simple_kernel, dim3(cdiv(a.n, SM_T), a.num_groups, row_tiles), 256, 0, stream, a), "fp8_matmul launch");
+  if (a.ld_a >= (int64_t)1 << 40 || a.ld_b >= (int64_t)1 << 40 || a.b_group >= (int64_t)1 << 40)
+    return set_last_error(TS_MOE_EUNSUPPORTED, "fp8_matmul: a stride of 2^40 or more");
+
+  const MatmulDevice* d = nullptr;
+  const ts_moe_status st = matmul_setup(&d);
+  if (st != TS_MOE_OK) return st;
+  const MatmulPlan plan = matmul_plan(a, d->sms);
+  MatmulParams p;
+  p.a = a;
+  p.kb = cdiv(a.k, SCALE_BLOCK);
+  p.splits = plan.splits;
+  // strides no row or matrix follows may be anything: give the map valid ones
+  const int64_t row = (a.k + 15) / 16 * 16, ld_a = a.rows > 1 ? a.ld_a : row, ld_b = a.n > 1 ? a.ld_b : row;
+  const int64_t group = a.num_groups > 1 ? a.b_group : (int64_t)a.n * ld_b;
+  CUtensorMap ma, mb;
+  if (!encode_rows(&ma, a.a, a.k, a.rows, ld_a, -1, 0, plan.box_a) || !encode_rows(&mb, a.b, a.k, a.n, ld_b, a.num_groups, group, plan.box_b))
+    return set_last_error(TS_MOE_ECUDA, "fp8_matmul: the driver refused a tensor map");
+  cudaError_t e;
+  if (plan.bt == 0)
+    e = launch(fp8_tile_kernel, dim3(plan.grid), TL_THREADS, tile_smem(), stream, p, ma, mb);
+  else if (plan.bt == 16)
+    e = launch_stream<16>(p, ma, mb, plan.grid, stream);
+  else if (plan.bt == 32)
+    e = launch_stream<32>(p, ma, mb, plan.grid, stream);
+  else if (plan.bt == 64)
+    e = launch_stream<64>(p, ma, mb, plan.grid, stream);
+  else
+    e = launch_stream<128>(p, ma, mb, plan.grid, stream);
+  return done(e, "fp8_matmul launch");
 }
 
 static int balance_ctas(int rows, int experts) {

@@ -173,7 +173,8 @@ def test_fp8_matmul(B, M, N, K):
     check_matmul(B, M, N, K, (BF16, FP16, FP32)[(M + N) % 3], add=(None, True, "in place")[(M + K) % 3])
 
 
-@pytest.mark.parametrize("M,N,K", [(1, 4096, 4096), (16, 5760, 2880), (3, 512, 14336), (2000, 1100, 300), (513, 4096, 1000)])
+@pytest.mark.parametrize("M,N,K", [(1, 4096, 4096), (16, 5760, 2880), (3, 512, 14336), (2000, 1100, 300), (513, 4096, 1000), (4100, 1300, 300),
+                                   (2500, 2049, 1), (2500, 2303, 129), (19000, 64, 1408), (700, 8200, 640)])
 def test_fp8_matmul_larger(B, M, N, K):
     check_matmul(B, M, N, K, BF16)
 
@@ -260,6 +261,7 @@ def grouped(B, sizes, N, K, out_type, tail=0, add=False, offsets=None, seed=0):
     ([3, 0, 1, 17, 0], 300, 200, 2), ([0, 0, 0], 64, 128, 5), ([1], 128, 64, 0), ([0, 40], 130, 1408, 0),
     ([129, 0, 256, 1, 400], 520, 390, 3), ([700, 5], 257, 256, 0), ([2] * 32, 576, 288, 0), ([1] * 256, 64, 64, 1),
     ([0] * 200 + [300] + [0] * 50, 384, 129, 0), ([64] * 8, 1000, 640, 0), ([100, 700, 90, 128, 0, 130], 768, 512, 50),
+    ([500, 0, 1300, 129, 2000, 3], 1300, 300, 9), ([0, 3000, 1, 700], 2049, 260, 1), ([128, 256, 384, 2100], 1800, 128, 0),
 ])
 def test_fp8_matmul_grouped(B, sizes, N, K, tail):
     grouped(B, sizes, N, K, (BF16, FP32, FP16)[len(sizes) % 3], tail=tail, add=len(sizes) % 2 == 0)
