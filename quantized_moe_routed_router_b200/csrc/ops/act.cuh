@@ -8,22 +8,23 @@ namespace tsm {
 
 constexpr int ACT_THREADS = 256;
 
-TSM_DEV float sigmoid_f(float x) { return __fdividef(1.f, 1.f + expf(-x)); }
+// 1 / (1 + 2^(-x log2 e)).  The exponent's rounding is off by |x| 2^-24 relative, which shows only where the
+// sigmoid itself is small; four instructions, two of them on the special-function unit, whose rate would
+// otherwise come to bound the kernel before HBM does.
+TSM_DEV float sigmoid_f(float x) { return rcp(1.f + ex2(-LOG2E * x)); }
 
-// Sixteen lanes per (row, group) unit, eight columns each; units row-major.
+// A warp takes two neighbouring groups of a row (its halves, eight columns a lane) at a time; pairs row-major.
+// step_rows, step_pairs: the grid's warps as whole rows of pairs and the rest, so that the loop divides nothing.
 template <bool VEC>
-__global__ void __launch_bounds__(ACT_THREADS) act_quant_kernel(const ts_moe_act_quant_args a) {
+__global__ void __launch_bounds__(ACT_THREADS) act_quant_kernel(const ts_moe_act_quant_args a, int pairs, int step_rows, int step_pairs) {
   grid_dep_wait();
   grid_dep_launch();
-  const int groups = cdiv(a.inter, SCALE_BLOCK);
-  const int64_t units = (int64_t)a.rows * groups;
-  const int lane = threadIdx.x & 15;
-  // both halves of a warp take every step together: the shuffles name all lanes
-  for (int64_t u0 = ((int64_t)blockIdx.x * ACT_THREADS + threadIdx.x) / 32 * 2; u0 < units; u0 += (int64_t)gridDim.x * (ACT_THREADS / 16)) {
-    const int64_t u = u0 + ((threadIdx.x >> 4) & 1);
-    const int64_t row = u / groups;
-    const int group = (int)(u - row * groups), col = group * SCALE_BLOCK + lane * 8;
-    const int n = u < units ? min(8, a.inter - col) : 0;
+  const unsigned w = blockIdx.x * (ACT_THREADS / 32) + (threadIdx.x >> 5);
+  int64_t row = w / (unsigned)pairs;
+  int pair = (int)(w - (unsigned)row * (unsigned)pairs);
+  while (row < a.rows) {
+    const int group = pair * 2 + ((threadIdx.x >> 4) & 1), col = group * SCALE_BLOCK + (threadIdx.x & 15) * 8;
+    const int n = min(8, a.inter - col);
     float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
     if (n > 0) {
       const Raw8 rg = load_raw8<VEC>(a.gate, a.in_type, row * a.ld_gate + col, n);
@@ -45,6 +46,12 @@ __global__ void __launch_bounds__(ACT_THREADS) act_quant_kernel(const ts_moe_act
       }
     }
     quant_group16<VEC>(v, a.q, row * a.ld_q + col, n, a.q_scale + row * a.qs_row + (int64_t)group * a.qs_group);
+    row += step_rows;
+    pair += step_pairs;
+    if (pair >= pairs) {
+      pair -= pairs;
+      ++row;
+    }
   }
 }
 

@@ -4,8 +4,8 @@
 //   dlogits[t][e] = dloss coef / T  p[t][e] s[t][e] (f[e] - sum_j f[j] p[t][j])
 //
 // with s = 1 for p = softmax(l), and s = 1 - sigmoid(l) for p = sigmoid(l) / sum
-// sigmoid(l).  The latter is computed as softmax(log sigmoid(l)): the same value,
-// and no sum of sigmoids that underflows for a row of very negative logits.
+// sigmoid(l).  There every sigmoid of a row is taken times e^-m, m = min(max l, 0),
+// which the quotient cancels: no sum underflows for a row of very negative logits.
 //
 // The gradient needs all counts, and the counts need idx only: the counts come
 // first (idx is a small share of the bytes), then one pass over the logits forms
@@ -17,10 +17,11 @@
 
 namespace tsm {
 
-constexpr int BAL_THREADS = 256, BAL_WARPS = BAL_THREADS / 32;
+constexpr int BAL_ALONE = 256, BAL_THREADS = 1024;  // threads of the only CTA, and of many: 32 warps a SM to hide the loads
+constexpr int BAL_WARPS = BAL_THREADS / 32;
 constexpr int BAL_MAX_E = TS_MOE_MAX_EXPERTS;
-constexpr int BAL_MAX_CTAS = 592;  // four per SM: part of the workspace's size, so fixed
-static_assert(BAL_MAX_E <= BAL_THREADS, "one thread per expert in the finish");
+constexpr int BAL_MAX_CTAS = 148;  // one per SM: part of the workspace's size, so fixed
+static_assert(BAL_MAX_E <= BAL_ALONE, "one thread per expert in the finish");
 
 // Head of the workspace; the CTAs' probability sums [CTAs][E] follow it.
 struct BalanceHead {
@@ -47,7 +48,7 @@ __host__ __device__ inline int balance_lanes(int E) {  // lanes that share a row
 // Adds rows [r0, r1) to the CTA's histogram; hist[BAL_MAX_E] counts rows.
 TSM_DEV void balance_count(const ts_moe_balance_args& a, int r0, int r1, int* hist) {
   const int K = a.top_k;
-  for (int i = threadIdx.x; i < (r1 - r0) * K; i += BAL_THREADS) {
+  for (int i = threadIdx.x; i < (r1 - r0) * K; i += blockDim.x) {
     const int t = i / K, k = i - t * K;
     const int64_t row = r0 + t;
     if (a.mask && !a.mask[row]) continue;
@@ -59,7 +60,7 @@ TSM_DEV void balance_count(const ts_moe_balance_args& a, int r0, int r1, int* hi
 
 // Integer adds: their order does not change the counts.
 TSM_DEV void balance_publish_counts(const BalanceParams& p, const int* hist) {
-  for (int e = threadIdx.x; e <= BAL_MAX_E; e += BAL_THREADS)
+  for (int e = threadIdx.x; e <= BAL_MAX_E; e += blockDim.x)
     if (hist[e]) atomicAdd(e < BAL_MAX_E ? &p.head->counts[e] : &p.head->tokens, hist[e]);
 }
 
@@ -67,7 +68,7 @@ __global__ void __launch_bounds__(BAL_THREADS) balance_count_kernel(const Balanc
   __shared__ int hist[BAL_MAX_E + 1];
   grid_dep_wait();
   grid_dep_launch();
-  for (int e = threadIdx.x; e <= BAL_MAX_E; e += BAL_THREADS) hist[e] = 0;
+  for (int e = threadIdx.x; e <= BAL_MAX_E; e += blockDim.x) hist[e] = 0;
   __syncthreads();
   const int per = cdiv(p.a.rows, gridDim.x), r0 = min(p.a.rows, (int)blockIdx.x * per);
   balance_count(p.a, r0, min(p.a.rows, r0 + per), hist);
@@ -75,27 +76,55 @@ __global__ void __launch_bounds__(BAL_THREADS) balance_count_kernel(const Balanc
   balance_publish_counts(p, hist);
 }
 
+// Quads of one row as they lie in memory.
+template <int NV>
+struct RawRow {
+  uint4 q[NV];
+};
+
 // LPR lanes share a row, NV quads of logits each: quad v of lane l holds experts
 // (v LPR + l) 4 .. + 3.
+template <int LPR, int NV>
+TSM_DEV RawRow<NV> balance_load(const ts_moe_balance_args& a, int64_t row, int lane, bool live, bool vec) {
+  RawRow<NV> r;
+#pragma unroll
+  for (int v = 0; v < NV; ++v) {
+    const int e0 = (v * LPR + lane) * 4;
+    r.q[v] = make_uint4(0, 0, 0, 0);
+    if (!live || e0 >= a.experts) continue;
+    const int64_t off = row * a.ld_logits + e0;
+    if (!vec)
+      r.q[v] = load_raw8<false>(a.logits, a.dtype, off, min(4, a.experts - e0)).a;
+    else if (a.dtype == TS_DT_FP32)
+      r.q[v] = *(const uint4*)((const float*)a.logits + off);
+    else {
+      const uint2 w = *(const uint2*)((const uint16_t*)a.logits + off);
+      r.q[v].x = w.x, r.q[v].y = w.y;
+    }
+  }
+  return r;
+}
+
 template <int LPR, int NV>
 __global__ void __launch_bounds__(BAL_THREADS) balance_kernel(const BalanceParams p) {
   constexpr int N = 4 * NV;
   __shared__ int hist[BAL_MAX_E + 1];
   __shared__ float sums[BAL_WARPS][BAL_MAX_E];
-  __shared__ float red[BAL_WARPS];
+  __shared__ float red[BAL_MAX_E / 32];
   __shared__ int last;
   const ts_moe_balance_args& a = p.a;
   const int E = a.experts, tid = threadIdx.x, warp = tid >> 5, lane = tid & (LPR - 1), sub = (tid & 31) / LPR;
+  const int warps = blockDim.x >> 5;
   grid_dep_wait();
   grid_dep_launch();
   const bool alone = gridDim.x == 1;
   const int per = cdiv(a.rows, (int)gridDim.x);
   const int r0 = min(a.rows, (int)blockIdx.x * per), r1 = min(a.rows, r0 + per);
   if (p.counted) {
-    for (int e = tid; e <= BAL_MAX_E; e += BAL_THREADS) hist[e] = e < BAL_MAX_E ? p.head->counts[e] : p.head->tokens;
+    for (int e = tid; e <= BAL_MAX_E; e += blockDim.x) hist[e] = e < BAL_MAX_E ? p.head->counts[e] : p.head->tokens;
     __syncthreads();
   } else {
-    for (int e = tid; e <= BAL_MAX_E; e += BAL_THREADS) hist[e] = 0;
+    for (int e = tid; e <= BAL_MAX_E; e += blockDim.x) hist[e] = 0;
     __syncthreads();
     balance_count(a, r0, r1, hist);
     __syncthreads();
@@ -112,63 +141,59 @@ __global__ void __launch_bounds__(BAL_THREADS) balance_kernel(const BalanceParam
     f[i] = e < E && T > 0 ? (float)hist[e] * ((float)E / ((float)a.top_k * (float)T)) : 0.f;
     psum[i] = 0.f;
   }
-  const int es = dt_size(a.dtype);
-  const bool vec = ((uintptr_t)a.logits | (uintptr_t)(a.ld_logits * es)) % 16 == 0 && E % 4 == 0;
-  const bool vec_out = ((uintptr_t)a.dlogits | (uintptr_t)(a.ld_dlogits * es)) % 16 == 0 && E % 4 == 0;
+  const int align = a.dtype == TS_DT_FP32 ? 16 : 8, es = dt_size(a.dtype);
+  const bool vec = ((uintptr_t)a.logits | (uintptr_t)(a.ld_logits * es)) % align == 0 && E % 4 == 0;
+  const bool vec_out = ((uintptr_t)a.dlogits | (uintptr_t)(a.ld_dlogits * es)) % align == 0 && E % 4 == 0;
+  const int step = warps * (32 / LPR);
   // every lane of a warp takes every step: the shuffles name all of them
-  for (int rb = r0 + warp * (32 / LPR); rb < r1; rb += BAL_WARPS * (32 / LPR)) {
-    const int64_t row = rb + sub;
-    const bool in = row < r1, live = in && (!a.mask || a.mask[row]);
-    float x[N], t[N], m = -INFINITY;
+  int64_t row = r0 + warp * (32 / LPR) + sub;
+  bool live = row < r1 && (!a.mask || a.mask[row]);
+  RawRow<NV> raw = balance_load<LPR, NV>(a, row, lane, live, vec);
+  for (int rb = r0 + warp * (32 / LPR); rb < r1; rb += step) {
+    const RawRow<NV> now = raw;
+    const int64_t at = row;
+    const bool in = at < r1, on = live;
+    row += step;  // the next row's loads run while this one is worked on
+    live = row < r1 && (!a.mask || a.mask[row]);
+    raw = balance_load<LPR, NV>(a, row, lane, live, vec);
+    float t[N], m = -INFINITY;
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
-      const int e0 = (v * LPR + lane) * 4;
-#pragma unroll
-      for (int j = 0; j < 4; ++j) x[4 * v + j] = -INFINITY;
-      if (live && e0 < E) {
-        const int64_t off = row * a.ld_logits + e0;
-        if (a.dtype == TS_DT_FP32) {
-          const float* q = (const float*)a.logits + off;
-          if (vec) {
-            const float4 w = *(const float4*)q;
-            x[4 * v] = w.x, x[4 * v + 1] = w.y, x[4 * v + 2] = w.z, x[4 * v + 3] = w.w;
-          } else {
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-              if (e0 + j < E) x[4 * v + j] = q[j];
-          }
-        } else {
-          const uint16_t* q = (const uint16_t*)a.logits + off;
-          Raw8 r;
-          r.a = make_uint4(0, 0, 0, 0);
-          if (vec) {
-            const uint2 w = *(const uint2*)q;
-            r.a.x = w.x, r.a.y = w.y;
-          } else {
-            r = load_raw8<false>(a.logits, a.dtype, off, min(4, E - e0));
-          }
-          float w8[8];
-          cvt8(r, a.dtype, w8);
-#pragma unroll
-          for (int j = 0; j < 4; ++j)
-            if (e0 + j < E) x[4 * v + j] = w8[j];
-        }
-      }
+      Raw8 r;
+      r.a = now.q[v];
+      r.b = make_uint4(0, 0, 0, 0);
+      float w[8];
+      cvt8(r, a.dtype, w);
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const float l = x[4 * v + j];
-        // log sigmoid(l) = min(l, 0) - log(1 + exp(-|l|))
-        t[4 * v + j] = a.score == TS_SCORE_SIGMOID_RENORM ? fminf(l, 0.f) - log1pf(expf(-fabsf(l))) : l;
+        const int e = (v * LPR + lane) * 4 + j;
+        t[4 * v + j] = on && e < E ? w[j] : -INFINITY;
         m = fmaxf(m, t[4 * v + j]);
       }
     }
 #pragma unroll
     for (int d = LPR / 2; d >= 1; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, d));
     if (m == -INFINITY) m = 0.f;  // nothing left in the row: p = 0
-    float s = 0.f, fp = 0.f;
+    float slope[N], s = 0.f, fp = 0.f;
+    if (a.score == TS_SCORE_SIGMOID_RENORM) {
+      const float low = fminf(m, 0.f);
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        // u = e^-|l|: sigmoid(l) = (l >= 0 ? 1 : u) / (1 + u), 1 - sigmoid(l) = (l >= 0 ? u : 1) / (1 + u)
+        const float l = t[i], u = ex2(-LOG2E * fabsf(l)), d = rcp(1.f + u);
+        const float e = low < 0.f ? ex2(LOG2E * (l - low)) : u;  // e^(l - low), for l < 0
+        slope[i] = l >= 0.f ? u * d : d;
+        t[i] = l >= 0.f ? d : e * d;
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        t[i] = ex2(LOG2E * (t[i] - m));
+        slope[i] = 1.f;
+      }
+    }
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-      t[i] = expf(t[i] - m);
       s += t[i];
       fp += f[i] * t[i];
     }
@@ -182,7 +207,7 @@ __global__ void __launch_bounds__(BAL_THREADS) balance_kernel(const BalanceParam
 #pragma unroll
     for (int i = 0; i < N; ++i) {
       t[i] *= inv;
-      if (live) psum[i] += t[i];
+      if (on) psum[i] += t[i];
     }
     if (a.dlogits && in) {
 #pragma unroll
@@ -190,15 +215,10 @@ __global__ void __launch_bounds__(BAL_THREADS) balance_kernel(const BalanceParam
         const int e0 = (v * LPR + lane) * 4;
         float g[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int i = 4 * v + j;
-          if (live) {
-            g[j] = gscale * t[i] * (f[i] - fp);
-            if (a.score == TS_SCORE_SIGMOID_RENORM) g[j] *= 1.f / (1.f + expf(x[i]));
-          }
-        }
+        for (int j = 0; j < 4; ++j)
+          if (on) g[j] = gscale * t[4 * v + j] * (f[4 * v + j] - fp) * slope[4 * v + j];
         if (e0 < E) {
-          const int64_t off = row * a.ld_dlogits + e0;
+          const int64_t off = at * a.ld_dlogits + e0;
           const Raw8 r = round8(g, a.dtype);
           if (!vec_out)
             store_raw8<false>(a.dlogits, a.dtype, off, min(4, E - e0), r);
@@ -222,7 +242,7 @@ __global__ void __launch_bounds__(BAL_THREADS) balance_kernel(const BalanceParam
   __syncthreads();
   float P = 0.f;
   if (tid < E)
-    for (int w = 0; w < BAL_WARPS; ++w) P += sums[w][tid];
+    for (int w = 0; w < warps; ++w) P += sums[w][tid];
   if (!alone) {
     if (tid < E) p.part[(int64_t)blockIdx.x * E + tid] = P;
     __threadfence();
@@ -231,11 +251,19 @@ __global__ void __launch_bounds__(BAL_THREADS) balance_kernel(const BalanceParam
     __syncthreads();
     if (!last) return;
     __threadfence();
-    P = 0.f;
-    if (tid < E) {
-      for (int b = 0; b < (int)gridDim.x; ++b) P += ld_cg(&p.part[(int64_t)b * E + tid]);
+    // the CTAs' sums: four threads an expert where there are four, CTAs a stride apart, many loads in flight
+    const int segs = (int)blockDim.x / BAL_MAX_E, seg = tid / BAL_MAX_E, e = tid % BAL_MAX_E;
+    float part = 0.f;
+    if (e < E) {
+#pragma unroll 8
+      for (int b = seg; b < (int)gridDim.x; b += segs) part += __ldcg(&p.part[(int64_t)b * E + e]);
     }
-    for (int e = tid; e <= BAL_MAX_E; e += BAL_THREADS)
+    sums[seg][e] = part;
+    __syncthreads();
+    P = 0.f;
+    if (tid < E)
+      for (int w = 0; w < segs; ++w) P += sums[w][tid];
+    for (int e = tid; e <= BAL_MAX_E; e += blockDim.x)
       hist[e] = (int)__ldcg((const unsigned*)(e < BAL_MAX_E ? &p.head->counts[e] : &p.head->tokens));
     __syncthreads();
   }
@@ -252,7 +280,7 @@ __global__ void __launch_bounds__(BAL_THREADS) balance_kernel(const BalanceParam
   }
 #pragma unroll
   for (int d = 16; d >= 1; d >>= 1) term += __shfl_xor_sync(0xFFFFFFFFu, term, d);
-  if ((tid & 31) == 0) red[warp] = term;
+  if ((tid & 31) == 0 && tid < BAL_MAX_E) red[warp] = term;
   int run = count;
 #pragma unroll
   for (int d = 1; d < 32; d <<= 1) {
@@ -260,9 +288,9 @@ __global__ void __launch_bounds__(BAL_THREADS) balance_kernel(const BalanceParam
     if ((tid & 31) >= d) run += o;
   }
   __syncthreads();
-  if ((tid & 31) == 31) hist[warp] = run;  // the counts are in registers by now
+  if ((tid & 31) == 31 && tid < BAL_MAX_E) hist[warp] = run;  // the counts are in registers by now
   __syncthreads();
-  if (a.offsets) {
+  if (a.offsets && tid < BAL_MAX_E) {
     int base = 0;
     for (int w = 0; w < warp; ++w) base += hist[w];
     if (tid < E) a.offsets[tid + 1] = base + run;
@@ -270,7 +298,7 @@ __global__ void __launch_bounds__(BAL_THREADS) balance_kernel(const BalanceParam
   }
   if (tid == 0) {
     float loss = 0.f;
-    for (int w = 0; w < BAL_WARPS; ++w) loss += red[w];
+    for (int w = 0; w < BAL_MAX_E / 32; ++w) loss += red[w];
     *a.loss = a.coef * loss;
   }
 }

@@ -121,6 +121,20 @@ TSM_DEV void store_raw8(void* base, int type, int64_t off, int n, const Raw8& r)
   }
 }
 
+constexpr float LOG2E = 1.4426950408889634f;
+
+// 2^x and 1 / x by the special-function unit (each within 2 ulp); 2^x is 0 below the normal range.
+TSM_DEV float ex2(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+TSM_DEV float rcp(float x) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
 // Maximum that keeps a NaN (fmaxf drops it).
 TSM_DEV float max_nan(float a, float b) {
   float r;

@@ -10,13 +10,15 @@
 
 namespace tsm {
 
-constexpr int NORM_MAX_THREADS = 1024;
+// Threads of the largest row's CTA: one or two chunks per thread for few rows, four for many.
+template <int IT>
+constexpr int NORM_MAX_THREADS = IT == 4 ? 512 : 1024;
 
 // One CTA per row; thread t holds the eight-column chunks t, t + blockDim.x, ...
 // (IT of them), so sixteen neighbouring lanes hold one 128-column scale group.
 template <int IT, bool VEC>
-__global__ void __launch_bounds__(NORM_MAX_THREADS) rmsnorm_kernel(const ts_moe_rmsnorm_args a) {
-  __shared__ float warp_sum[NORM_MAX_THREADS / 32];
+__global__ void __launch_bounds__(NORM_MAX_THREADS<IT>) rmsnorm_kernel(const ts_moe_rmsnorm_args a) {
+  __shared__ float warp_sum[NORM_MAX_THREADS<IT> / 32];
   grid_dep_wait();
   grid_dep_launch();
   const int64_t row = blockIdx.x;

@@ -222,9 +222,13 @@ ts_moe_status ts_moe_act_quant(const ts_moe_act_quant_args* args, void* stream) 
   if (a.ld_gate < a.inter || a.ld_up < a.inter || a.ld_q < a.inter) return bad("act_quant: a row stride is smaller than inter");
   const bool vec = a.inter % 8 == 0 && aligned_rows(a.gate, a.ld_gate, a.in_type) && aligned_rows(a.up, a.ld_up, a.in_type) &&
                    aligned(a.q, a.ld_q, 8);
-  const int64_t units = (int64_t)a.rows * cdiv(a.inter, SCALE_BLOCK);
-  const int grid = (int)std::min<int64_t>((units + ACT_THREADS / 16 - 1) / (ACT_THREADS / 16), 148 * 8);
-  return done(launch(vec ? act_quant_kernel<true> : act_quant_kernel<false>, dim3(grid), ACT_THREADS, 0, stream, a), "act_quant launch");
+  const int pairs = cdiv(a.inter, 2 * SCALE_BLOCK);
+  const int64_t units = (int64_t)a.rows * pairs;
+  const int grid = (int)std::min<int64_t>((units + ACT_THREADS / 32 - 1) / (ACT_THREADS / 32), 148 * 8);
+  const int warps = grid * (ACT_THREADS / 32);
+  return done(launch(vec ? act_quant_kernel<true> : act_quant_kernel<false>, dim3(grid), ACT_THREADS, 0, stream, a, pairs, warps / pairs,
+                     warps % pairs),
+              "act_quant launch");
 }
 
 ts_moe_status ts_moe_fp8_matmul(const ts_moe_fp8_matmul_args* args, void* stream) {
@@ -275,8 +279,8 @@ ts_moe_status ts_moe_fp8_matmul(const ts_moe_fp8_matmul_args* args, void* stream
 }
 
 static int balance_ctas(int rows, int experts) {
-  const int rows_per_pass = BAL_WARPS * (32 / balance_lanes(experts));
-  return std::min(cdiv(std::max(rows, 1), rows_per_pass * 4), BAL_MAX_CTAS);
+  if ((int64_t)rows * experts <= 16384) return 1;
+  return std::min(cdiv(rows, BAL_WARPS * (32 / balance_lanes(experts))), BAL_MAX_CTAS);
 }
 
 uint64_t ts_moe_balance_workspace(int32_t rows, int32_t experts) {
@@ -308,15 +312,14 @@ ts_moe_status ts_moe_balance(const ts_moe_balance_args* args, void* stream) {
   p.head = (BalanceHead*)a.workspace;
   p.part = (float*)((char*)a.workspace + sizeof(BalanceHead));
   const int lanes = balance_lanes(a.experts);
-  int ctas = balance_ctas(a.rows, a.experts);
-  if ((int64_t)a.rows * a.experts <= 16384) ctas = 1;
+  const int ctas = balance_ctas(a.rows, a.experts);
   p.counted = ctas > 1 && a.dlogits ? 1 : 0;
   if (ctas > 1) {
     const cudaError_t e = cudaMemsetAsync(p.head, 0, sizeof(BalanceHead), (cudaStream_t)stream);
     if (e != cudaSuccess) return cuda_bad(e, "balance workspace");
   }
   if (p.counted) {
-    const int n = std::min(cdiv(a.rows * a.top_k, BAL_THREADS * 8), 148);
+    const int n = std::min(cdiv(a.rows * a.top_k, BAL_THREADS * 2), 148);
     const cudaError_t e = launch(balance_count_kernel, dim3(n), BAL_THREADS, 0, stream, p);
     if (e != cudaSuccess) return cuda_bad(e, "balance count launch");
   }
@@ -326,7 +329,7 @@ ts_moe_status ts_moe_balance(const ts_moe_balance_args* args, void* stream) {
            : lanes == 16 ? balance_kernel<16, 1>
            : a.experts <= 128 ? balance_kernel<32, 1>
                               : balance_kernel<32, 2>;
-  return done(launch(k, dim3(ctas), BAL_THREADS, 0, stream, p), "balance launch");
+  return done(launch(k, dim3(ctas), ctas == 1 ? BAL_ALONE : BAL_THREADS, 0, stream, p), "balance launch");
 }
 
 }  // extern "C"
