@@ -75,6 +75,42 @@ TSM_DEV void cvt8(const Raw8& r, int type, float (&v)[8]) {
   }
 }
 
+// The same where the kernel's instance knows the width: eight 16-bit elements take one uint4.
+template <bool WIDE>
+struct Raw;
+template <>
+struct Raw<false> {
+  uint4 a;
+};
+template <>
+struct Raw<true> {
+  uint4 a, b;
+};
+// Eight elements at a 16-byte boundary; streamed: each is read once.
+template <bool WIDE>
+TSM_DEV Raw<WIDE> load_vec(const void* base, int64_t off) {
+  Raw<WIDE> r;
+  if constexpr (WIDE) {
+    const uint4* p = (const uint4*)((const float*)base + off);
+    r.a = __ldcs(p);
+    r.b = __ldcs(p + 1);
+  } else {
+    r.a = __ldcs((const uint4*)((const uint16_t*)base + off));
+  }
+  return r;
+}
+template <bool WIDE>
+TSM_DEV void cvt_vec(const Raw<WIDE>& r, int type, float (&v)[8]) {
+  Raw8 w;
+  w.a = r.a;
+  if constexpr (WIDE) {
+    w.b = r.b;
+    cvt8(w, TS_DT_FP32, v);
+  } else {
+    cvt8(w, type == TS_DT_BF16 ? TS_DT_BF16 : TS_DT_FP16, v);
+  }
+}
+
 TSM_DEV uint32_t pack2(float x, float y, int type) {
   if (type == TS_DT_BF16) {
     const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
@@ -142,39 +178,48 @@ TSM_DEV float max_nan(float a, float b) {
   return r;
 }
 
-// Sixteen neighbouring lanes hold the 128 columns of one group, eight each
-// (lanes past the row's end hold zeros).  Writes the group's E4M3 codes and,
-// from its first lane, its scale.  amax / 448 and its reciprocal are formed by
-// IEEE divisions; v * (1 / scale) differs from v / scale by under 2^-23
-// relative, which moves a code only where v / scale lies that close to the
-// middle between two codes.  The conversion saturates, so the group's largest
-// value lands on 448 whichever way that rounds.
-template <bool VEC>
-TSM_DEV void quant_group16(const float (&v)[8], uint8_t* q, int64_t off, int n, float* scale) {
-  float m = 0.f;
+// LANES neighbouring lanes hold the 128 columns of one group in chunks of eight
+// columns: chunk c of lane l stands at column (c LANES + l) 8 of the group (lanes
+// past the row's end hold zeros).  Writes the group's E4M3 codes and, from its
+// first lane, its scale.  amax / 448 is formed as a product with the rounded
+// reciprocal and the codes as products with rcp(scale), each within 2 ulp of the
+// quotient, which moves a code only where v / scale lies that close to the middle
+// between two codes; IEEE divisions here cost as many instructions as the eight
+// values of a lane.  The conversion saturates, so the group's largest value lands
+// on 448 whichever way that rounds.
+template <int LANES, bool VEC>
+TSM_DEV void quant_group(const float (&v)[16 / LANES][8], uint8_t* q, int64_t off, int n, float* scale) {
+  constexpr int C = 16 / LANES;
+  float m = AMAX_FLOOR;
 #pragma unroll
-  for (int j = 0; j < 8; ++j) m = max_nan(m, fabsf(v[j]));
+  for (int c = 0; c < C; ++c) {
 #pragma unroll
-  for (int d = 8; d >= 1; d >>= 1) m = max_nan(m, __shfl_xor_sync(0xFFFFFFFFu, m, d, 16));
-  const float s = max_nan(m, AMAX_FLOOR) / E4M3_MAX;
-  const float inv = 1.f / s;
-  uint32_t w[2];
-#pragma unroll
-  for (int j = 0; j < 2; ++j) {
-    const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(v[4 * j] * inv, v[4 * j + 1] * inv), __NV_SATFINITE, __NV_E4M3);
-    const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(v[4 * j + 2] * inv, v[4 * j + 3] * inv), __NV_SATFINITE, __NV_E4M3);
-    w[j] = lo | hi << 16;
+    for (int j = 0; j < 8; ++j) m = max_nan(m, fabsf(v[c][j]));
   }
-  if (n > 0) {
+#pragma unroll
+  for (int d = LANES / 2; d >= 1; d >>= 1) m = max_nan(m, __shfl_xor_sync(0xFFFFFFFFu, m, d, LANES));
+  const float s = m * (1.f / E4M3_MAX);
+  const float inv = rcp(s);
+#pragma unroll
+  for (int c = 0; c < C; ++c) {
+    uint32_t w[2];
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(v[c][4 * j] * inv, v[c][4 * j + 1] * inv), __NV_SATFINITE, __NV_E4M3);
+      const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(v[c][4 * j + 2] * inv, v[c][4 * j + 3] * inv), __NV_SATFINITE, __NV_E4M3);
+      w[j] = lo | hi << 16;
+    }
+    const int64_t at = off + c * LANES * 8;
+    const int nc = n - c * LANES * 8;
     if (VEC) {
-      *(uint2*)(q + off) = make_uint2(w[0], w[1]);
+      if (nc > 0) *(uint2*)(q + at) = make_uint2(w[0], w[1]);
     } else {
 #pragma unroll
       for (int j = 0; j < 8; ++j)
-        if (j < n) q[off + j] = (uint8_t)(w[j / 4] >> (8 * (j % 4)));
+        if (j < nc) q[at + j] = (uint8_t)(w[j / 4] >> (8 * (j % 4)));
     }
-    if ((threadIdx.x & 15) == 0) *scale = s;
   }
+  if (n > 0 && (threadIdx.x & (LANES - 1)) == 0) *scale = s;
 }
 
 }  // namespace tsm

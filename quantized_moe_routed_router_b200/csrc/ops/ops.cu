@@ -170,12 +170,29 @@ MatmulPlan matmul_plan(const ts_moe_fp8_matmul_args& a, int sms) {
 
 ts_moe_status done(cudaError_t e, const char* what) { return e == cudaSuccess ? TS_MOE_OK : cuda_bad(e, what); }
 
-template <bool VEC>
-cudaError_t launch_norm(const ts_moe_rmsnorm_args& a, void* stream) {
+template <int PAIRS, int MAX_THREADS>
+cudaError_t launch_norm_rows(const ts_moe_rmsnorm_args& a, void* stream) {
+  const int threads = cdiv(cdiv(cdiv(a.hidden, SCALE_BLOCK), PAIRS) * 8, 32) * 32;
+  const bool rw = a.resid_type == TS_DT_FP32, dw = a.delta && a.delta_type == TS_DT_FP32;
+  auto k = rw ? (dw ? rmsnorm_rows_kernel<PAIRS, MAX_THREADS, true, true> : rmsnorm_rows_kernel<PAIRS, MAX_THREADS, true, false>)
+              : (dw ? rmsnorm_rows_kernel<PAIRS, MAX_THREADS, false, true> : rmsnorm_rows_kernel<PAIRS, MAX_THREADS, false, false>);
+  int per_sm = 1;
+  const cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, k, threads, 0);
+  if (e != cudaSuccess) return e;
+  return launch(k, dim3(std::min(a.rows, 148 * std::max(per_sm, 1))), threads, 0, stream, a);
+}
+
+cudaError_t launch_norm(const ts_moe_rmsnorm_args& a, bool vec, void* stream) {
   const int chunks = cdiv(a.hidden, 8);
+  if (vec && a.rows > 1024)
+    return a.hidden <= 4096   ? launch_norm_rows<1, 256>(a, stream)
+           : a.hidden <= 8192 ? launch_norm_rows<1, 512>(a, stream)
+                              : launch_norm_rows<2, 512>(a, stream);
   const int it = a.rows <= 1024 ? (chunks <= 1024 ? 1 : 2) : 4;
   const int threads = std::max(32, cdiv(cdiv(chunks, it), 32) * 32);
-  auto k = it == 1 ? rmsnorm_kernel<1, VEC> : it == 2 ? rmsnorm_kernel<2, VEC> : rmsnorm_kernel<4, VEC>;
+  auto k = it == 1   ? (vec ? rmsnorm_kernel<1, true> : rmsnorm_kernel<1, false>)
+           : it == 2 ? (vec ? rmsnorm_kernel<2, true> : rmsnorm_kernel<2, false>)
+                     : rmsnorm_kernel<4, false>;
   return launch(k, dim3(a.rows), threads, 0, stream, a);
 }
 
@@ -205,7 +222,7 @@ ts_moe_status ts_moe_rmsnorm(const ts_moe_rmsnorm_args* args, void* stream) {
                    aligned_rows(a.delta, a.ld_delta, a.delta_type) && aligned_rows(a.gamma, 0, a.gamma_type) &&
                    aligned_rows(a.resid_out, a.ld_resid_out, a.resid_type) && aligned_rows(a.y, a.ld_y, a.y_type) &&
                    (!a.q || aligned(a.q, a.ld_q, 8));
-  return done(vec ? launch_norm<true>(a, stream) : launch_norm<false>(a, stream), "rmsnorm launch");
+  return done(launch_norm(a, vec, stream), "rmsnorm launch");
 }
 
 ts_moe_status ts_moe_act_quant(const ts_moe_act_quant_args* args, void* stream) {
@@ -222,13 +239,14 @@ ts_moe_status ts_moe_act_quant(const ts_moe_act_quant_args* args, void* stream) 
   if (a.ld_gate < a.inter || a.ld_up < a.inter || a.ld_q < a.inter) return bad("act_quant: a row stride is smaller than inter");
   const bool vec = a.inter % 8 == 0 && aligned_rows(a.gate, a.ld_gate, a.in_type) && aligned_rows(a.up, a.ld_up, a.in_type) &&
                    aligned(a.q, a.ld_q, 8);
-  const int pairs = cdiv(a.inter, 2 * SCALE_BLOCK);
-  const int64_t units = (int64_t)a.rows * pairs;
-  const int grid = (int)std::min<int64_t>((units + ACT_THREADS / 32 - 1) / (ACT_THREADS / 32), 148 * 8);
+  const bool wide = a.in_type == TS_DT_FP32;
+  const int quads = cdiv(a.inter, 4 * SCALE_BLOCK);
+  const int64_t units = (int64_t)a.rows * quads;
+  const int resident = vec && wide ? 2 : 4;  // CTAs per SM by the kernel's launch bounds
+  const int grid = (int)std::min<int64_t>((units + ACT_THREADS / 32 - 1) / (ACT_THREADS / 32), 148 * resident);
   const int warps = grid * (ACT_THREADS / 32);
-  return done(launch(vec ? act_quant_kernel<true> : act_quant_kernel<false>, dim3(grid), ACT_THREADS, 0, stream, a, pairs, warps / pairs,
-                     warps % pairs),
-              "act_quant launch");
+  auto k = vec ? (wide ? act_quant_kernel<true, true> : act_quant_kernel<true, false>) : act_quant_kernel<false, false>;
+  return done(launch(k, dim3(grid), ACT_THREADS, 0, stream, a, quads, warps / quads, warps % quads), "act_quant launch");
 }
 
 ts_moe_status ts_moe_fp8_matmul(const ts_moe_fp8_matmul_args* args, void* stream) {
