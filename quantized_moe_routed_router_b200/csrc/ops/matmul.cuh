@@ -103,11 +103,16 @@ TSM_DEV void store1(void* p, int type, int64_t i, float v) {
 // ----------------------------------------------------------------------------- many rows
 constexpr int TL_M = 128, TL_N = 256, TL_STAGES = 4, TL_ACC = 2;  // TL_ACC x TL_N = all 512 columns of tensor memory
 constexpr int TL_BAND = 16;     // row tiles that run side by side over the columns: their rows of A stay in L2
-constexpr int TL_THREADS = 320; // producer warp, MMA warp, 8 warps that scale and add
+constexpr int TL_PARTS = 4, TL_COLS = TL_N / TL_PARTS;  // column parts of a tile: four warps scale and add one each
+constexpr int TL_ADDERS = 4 * TL_PARTS, TL_THREADS = 128 + 32 * TL_ADDERS;  // after the producer's and the MMAs' warpgroup
+// Registers a thread: at launch (what fits 640 threads), and as the two roles split them afterwards.
+constexpr int TL_REGS = 96, TL_REGS_ISSUE = 32, TL_REGS_ADD = 112;
+static_assert(128 * TL_REGS_ISSUE + 32 * TL_ADDERS * TL_REGS_ADD <= TL_THREADS * TL_REGS, "the split fits the launch's registers");
 
 struct TileSmem {
   uint8_t a[TL_STAGES][TL_M * SCALE_BLOCK];
   uint8_t b[TL_STAGES][TL_N * SCALE_BLOCK];
+  uint4 out[TL_ADDERS][32 * 4];  // a warp's 32 rows of 64 bytes on their way out
   uint64_t full[TL_STAGES], empty[TL_STAGES], acc_full[TL_ACC], acc_empty[TL_ACC], drain;
   uint32_t tmem;
   int dead;
@@ -139,17 +144,103 @@ TSM_DEV Tile locate_tile(const MatmulParams& p, const GroupTable& tab, int t) {
   return r;
 }
 
+// Rows row0 .. row0 + 31 (below hi), columns col0 .. of one warp: lane l holds row row0 + l.  They go out through
+// `stage`, 64 bytes of each row at a time, so that a store covers whole sectors of few rows instead of 16 bytes of 32;
+// 16-byte places within a row are permuted by the row's number, which spreads them over the banks both ways.
+TSM_DEV int stage_at(int r, int c) { return r * 4 + (c ^ (r >> 1 & 3)); }
+
+TSM_DEV void store_tile(const ts_moe_fp8_matmul_args& a, const float2 (&acc)[TL_COLS / 2], uint4* stage, int row0, int hi, int col0) {
+  const int lane = threadIdx.x & 31, type = a.out_type, es = dt_size(type), rows = min(32, hi - row0);
+  if (rows <= 0 || col0 >= a.n) return;  // uniform in the warp
+  const bool vec = ((uintptr_t)a.out | (uintptr_t)(a.ld_out * es)) % 16 == 0;
+  if (type != TS_DT_FP32 && !a.add && vec && col0 + TL_COLS <= a.n) {
+#pragma unroll
+    for (int h = 0; h < TL_COLS / 32; ++h) {
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        const float2* v = &acc[h * 16 + c * 4];
+        stage[stage_at(lane, c)] = make_uint4(pack2(v[0].x, v[0].y, type), pack2(v[1].x, v[1].y, type), pack2(v[2].x, v[2].y, type),
+                                              pack2(v[3].x, v[3].y, type));
+      }
+      __syncwarp();
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int r = i * 8 + lane / 4, c = lane % 4;
+        if (r < rows) *(uint4*)((uint16_t*)a.out + (int64_t)(row0 + r) * a.ld_out + col0 + h * 32 + c * 8) = stage[stage_at(r, c)];
+      }
+      __syncwarp();
+    }
+    return;
+  }
+  const bool vadd = ((uintptr_t)a.add | (uintptr_t)(a.ld_add * es)) % 16 == 0;
+#pragma unroll
+  for (int h = 0; h < TL_COLS / 16; ++h) {
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      const float2 x = acc[h * 8 + c * 2], y = acc[h * 8 + c * 2 + 1];
+      stage[stage_at(lane, c)] = make_uint4(__float_as_uint(x.x), __float_as_uint(x.y), __float_as_uint(y.x), __float_as_uint(y.y));
+    }
+    __syncwarp();
+    const int c0 = col0 + h * 16;
+    if (vec && vadd && c0 + 16 <= a.n) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int r = i * 8 + lane / 4, c = lane % 4;
+        if (r < rows) {
+          const uint4 w = stage[stage_at(r, c)];
+          float v[4] = {__uint_as_float(w.x), __uint_as_float(w.y), __uint_as_float(w.z), __uint_as_float(w.w)};
+          const int64_t out = (int64_t)(row0 + r) * a.ld_out + c0 + c * 4, add = (int64_t)(row0 + r) * a.ld_add + c0 + c * 4;
+          if (type == TS_DT_FP32) {
+            if (a.add) {
+              const float4 d = *(const float4*)((const float*)a.add + add);
+              v[0] += d.x, v[1] += d.y, v[2] += d.z, v[3] += d.w;
+            }
+            *(float4*)((float*)a.out + out) = make_float4(v[0], v[1], v[2], v[3]);
+          } else {
+            if (a.add) {
+              const uint2 d = *(const uint2*)((const uint16_t*)a.add + add);
+              Raw8 raw;
+              raw.a = make_uint4(d.x, d.y, 0, 0);
+              float f[8];
+              cvt8(raw, type, f);
+#pragma unroll
+              for (int j = 0; j < 4; ++j) v[j] += f[j];
+            }
+            *(uint2*)((uint16_t*)a.out + out) = make_uint2(pack2(v[0], v[1], type), pack2(v[2], v[3], type));
+          }
+        }
+      }
+    } else {
+      // odd places: sixteen columns of two rows at a time, element by element
+      const float* f = (const float*)stage;
+      const int c = lane % 16;
+#pragma unroll 4
+      for (int i = 0; i < 16; ++i) {
+        const int r = i * 2 + lane / 16;
+        if (r < rows && c0 + c < a.n) {
+          float v = f[stage_at(r, c / 4) * 4 + c % 4];
+          if (a.add) v += load1(a.add, type, (int64_t)(row0 + r) * a.ld_add + c0 + c);
+          store1(a.out, type, (int64_t)(row0 + r) * a.ld_out + c0 + c, v);
+        }
+      }
+    }
+    __syncwarp();
+  }
+}
+
 __global__ void __launch_bounds__(TL_THREADS, 1)
     fp8_tile_kernel(const MatmulParams p, const __grid_constant__ CUtensorMap ma, const __grid_constant__ CUtensorMap mb) {
+  // Without static shared memory the dynamic part starts at a 1024-byte boundary, as the swizzled tiles need it; were it
+  // otherwise, the CTA would be dead from the start and its outputs NaN.
   extern __shared__ uint8_t raw[];
-  TileSmem& s = *reinterpret_cast<TileSmem*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
+  TileSmem& s = *reinterpret_cast<TileSmem*>(raw);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   volatile int* dead = &s.dead;
   if (threadIdx.x == 0) {
     for (int i = 0; i < TL_STAGES; ++i) mbar_init(&s.full[i], 1), mbar_init(&s.empty[i], 1);
-    for (int i = 0; i < TL_ACC; ++i) mbar_init(&s.acc_full[i], 1), mbar_init(&s.acc_empty[i], 8);
+    for (int i = 0; i < TL_ACC; ++i) mbar_init(&s.acc_full[i], 1), mbar_init(&s.acc_empty[i], TL_ADDERS);
     mbar_init(&s.drain, 1);
-    s.dead = 0;
+    s.dead = (smem_addr(raw) & 1023) != 0;
     fence_barrier_init();
     prefetch_map(&ma);
     prefetch_map(&mb);
@@ -164,6 +255,7 @@ __global__ void __launch_bounds__(TL_THREADS, 1)
   const uint32_t tmem = s.tmem;
   const int tiles = s.groups.first[p.a.num_groups] * cdiv(p.a.n, TL_N);
 
+  if (warp < 4) set_regs_down<TL_REGS_ISSUE>();
   if (warp == 0) {
     if (lane == 0) {
       unsigned it = 0;
@@ -209,72 +301,53 @@ __global__ void __launch_bounds__(TL_THREADS, 1)
       while (!mbar_try_wait(&s.drain, 0) && globaltimer() - t0 < WAIT_LIMIT_NS) {
       }
     }
-  } else {
-    const int quarter = warp & 3, half = (warp - 2) >> 2;
-    const uint32_t mine = tmem + ((uint32_t)(quarter * 32) << 16) + half * 128;
+  } else if (warp >= 4) {
+    set_regs_up<TL_REGS_ADD>();
+    const int quarter = warp & 3, part = (warp - 4) >> 2;
+    const uint32_t mine = tmem + ((uint32_t)(quarter * 32) << 16) + part * TL_COLS;
     const int nblocks = cdiv(p.a.n, SCALE_BLOCK);
     unsigned it = 0;
     for (int t = blockIdx.x; t < tiles; t += gridDim.x) {
       const Tile tl = locate_tile(p, s.groups, t);
-      const int row = tl.m0 + quarter * 32 + lane, col0 = tl.n0 + half * 128;
-      const float* sa = p.a.a_scale + (int64_t)min(row, tl.hi - 1) * p.a.as_row;
+      const int row0 = tl.m0 + quarter * 32, col0 = tl.n0 + part * TL_COLS;
+      const float* sa = p.a.a_scale + (int64_t)min(row0 + lane, tl.hi - 1) * p.a.as_row;
       const float* sb = p.a.b_scale + tl.g * p.a.bs_group + (int64_t)min(col0 / SCALE_BLOCK, nblocks - 1) * p.a.bs_row;
-      float acc[128];
+      float2 acc[TL_COLS / 2];
 #pragma unroll
-      for (int j = 0; j < 128; ++j) acc[j] = 0.f;
-      float na = *sa, nb = *sb;
+      for (int j = 0; j < TL_COLS / 2; ++j) acc[j] = make_float2(0.f, 0.f);
+      // the scales of two blocks ahead are on their way
+      float na = *sa, nb = *sb, ma2 = 0.f, mb2 = 0.f;
+      if (p.kb > 1) ma2 = sa[p.a.as_block], mb2 = sb[p.a.bs_block];
       for (int c = 0; c < p.kb; ++c, ++it) {
         const int ac = it % TL_ACC;
         const float sc = na * nb;
-        if (c + 1 < p.kb) {
-          na = sa[(int64_t)(c + 1) * p.a.as_block];
-          nb = sb[(int64_t)(c + 1) * p.a.bs_block];
+        na = ma2, nb = mb2;
+        if (c + 2 < p.kb) {
+          ma2 = sa[(int64_t)(c + 2) * p.a.as_block];
+          mb2 = sb[(int64_t)(c + 2) * p.a.bs_block];
         }
         wait_or_die(&s.acc_full[ac], it / TL_ACC & 1, dead);  // a dead CTA runs on without waiting
         __syncwarp();
         tc_fence_after();
-        float v[2][16];
-        tmem_ld16(mine + ac * TL_N, v[0]);
 #pragma unroll
-        for (int q = 0; q < 8; ++q) {
-          tc_wait_ld(v[q & 1]);
-          if (q < 7) tmem_ld16(mine + ac * TL_N + (q + 1) * 16, v[(q + 1) & 1]);
-#pragma unroll
-          for (int j = 0; j < 16; ++j) acc[q * 16 + j] += sc * v[q & 1][j];
-        }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&s.acc_empty[ac]);
-      }
-      if (row < tl.hi) {
-        const bool lost = *dead;
-        const int type = p.a.out_type, n = min(128, p.a.n - col0);
-        const bool vec = ((uintptr_t)p.a.out | (uintptr_t)(p.a.ld_out * dt_size(type))) % 16 == 0;
-        const bool vadd = ((uintptr_t)p.a.add | (uintptr_t)(p.a.ld_add * dt_size(type))) % 16 == 0;
-#pragma unroll
-        for (int q = 0; q < 16; ++q) {
-          const int w = min(8, n - q * 8);
-          if (w > 0) {
-            const int64_t col = col0 + q * 8;
-            float v[8];
-#pragma unroll
-            for (int j = 0; j < 8; ++j) v[j] = lost ? NAN : acc[q * 8 + j];
-            if (p.a.add) {
-              const int64_t off = (int64_t)row * p.a.ld_add + col;
-              const Raw8 r = vadd && w == 8 ? load_raw8<true>(p.a.add, type, off, 8) : load_raw8<false>(p.a.add, type, off, w);
-              float d[8];
-              cvt8(r, type, d);
-#pragma unroll
-              for (int j = 0; j < 8; ++j) v[j] += d[j];
-            }
-            const int64_t off = (int64_t)row * p.a.ld_out + col;
-            if (vec && w == 8)
-              store_raw8<true>(p.a.out, type, off, 8, round8(v, type));
-            else
-              store_raw8<false>(p.a.out, type, off, w, round8(v, type));
+        for (int q = 0; q < TL_COLS / 32; ++q) {
+          float v[32];
+          tmem_ld32(mine + ac * TL_N + q * 32, v);
+          tc_wait_ld32(v);
+          if (q == TL_COLS / 32 - 1) {  // all read: the MMAs may write here again
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&s.acc_empty[ac]);
           }
+#pragma unroll
+          for (int j = 0; j < 16; ++j) fma2(acc[q * 16 + j], sc, v[2 * j], v[2 * j + 1]);
         }
       }
+      if (*dead) {
+#pragma unroll
+        for (int j = 0; j < TL_COLS / 2; ++j) acc[j] = make_float2(NAN, NAN);
+      }
+      store_tile(p.a, acc, s.out[warp - 4], row0, tl.hi, col0);
     }
   }
   __syncwarp();
@@ -328,13 +401,17 @@ __global__ void __launch_bounds__(ST_THREADS, StreamShape<BT>::CTAS)
     prefetch_map(&mb);
   }
   if (warp == 1) tmem_alloc<S::COLS>(&s.tmem);
-  grid_dep_wait();
-  grid_dep_launch();
-  if (warp == 0) fill_groups(p.a, BT, s.groups);
+  if (warp == 0 && !p.a.offsets) fill_groups(p.a, BT, s.groups);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   cluster_sync();  // the peers' barriers are ready
+  grid_dep_wait();
+  grid_dep_launch();
+  if (p.a.offsets) {
+    if (warp == 0) fill_groups(p.a, BT, s.groups);
+    __syncthreads();
+  }
   const uint32_t tmem = s.tmem;
   const int nt = cdiv(p.a.n, ST_N);
   const int items = s.groups.first[p.a.num_groups] * nt;
@@ -447,13 +524,15 @@ __global__ void __launch_bounds__(ST_THREADS, StreamShape<BT>::CTAS)
       if (splits == 1) {
         const bool lost = *dead;
 #pragma unroll
-        for (int j = 0; j < BT; ++j) {
-          if (j < rows && n < p.a.n) {
-            const int64_t m = m0 + j;
-            float v = lost ? NAN : acc[j];
-            if (p.a.add) v += load1(p.a.add, type, m * p.a.ld_add + n);
-            store1(p.a.out, type, m * p.a.ld_out + n, v);
-          }
+        for (int j0 = 0; j0 < BT; j0 += 8) {
+          float d[8];
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            d[j] = p.a.add && j0 + j < rows && n < p.a.n ? load1(p.a.add, type, (int64_t)(m0 + j0 + j) * p.a.ld_add + n) : 0.f;
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            if (j0 + j < rows && n < p.a.n)
+              store1(p.a.out, type, (int64_t)(m0 + j0 + j) * p.a.ld_out + n, (lost ? NAN : acc[j0 + j]) + d[j]);
         }
         continue;
       }
@@ -467,15 +546,23 @@ __global__ void __launch_bounds__(ST_THREADS, StreamShape<BT>::CTAS)
       __syncwarp();
       const bool lost = *dead;
       const int j0 = rows * rank / splits, j1 = rows * (rank + 1) / splits;
-      for (int j = j0; j < j1; ++j) {
-        float v = 0.f;
-        for (int q = 0; q < splits; ++q) v += peer_load(peer_addr(smem_addr(&s.red[j][r]), q));
-        if (n < p.a.n) {
-          const int64_t m = m0 + j;
-          if (lost) v = NAN;
-          if (p.a.add) v += load1(p.a.add, type, m * p.a.ld_add + n);
-          store1(p.a.out, type, m * p.a.ld_out + n, v);
+      // eight rows at a time: their loads run side by side
+      for (int jb = j0; jb < j1; jb += 8) {
+        float v[8], d[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const bool in = jb + j < j1 && n < p.a.n;
+          d[j] = p.a.add && in ? load1(p.a.add, type, (int64_t)(m0 + jb + j) * p.a.ld_add + n) : 0.f;
+          v[j] = 0.f;
         }
+        for (int q = 0; q < splits; ++q) {
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            if (jb + j < j1) v[j] += peer_load(peer_addr(smem_addr(&s.red[jb + j][r]), q));
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          if (jb + j < j1 && n < p.a.n) store1(p.a.out, type, (int64_t)(m0 + jb + j) * p.a.ld_out + n, (lost ? NAN : v[j]) + d[j]);
       }
       __syncwarp();
       if (lane < splits) peer_arrive(peer_addr(smem_addr(&s.red_free), lane));

@@ -87,34 +87,32 @@ __global__ void __launch_bounds__(NORM_MAX_THREADS<IT>) rmsnorm_kernel(const ts_
       if (a.y) store_raw8<VEC>(a.y, a.y_type, row * a.ld_y + col, n, round8(v[i], a.y_type));
     }
     if (a.q)
-      quant_group<16, VEC>(*reinterpret_cast<const float(*)[1][8]>(&v[i]), a.q, row * a.ld_q + col, n, a.q_scale + row * a.qs_row + (int64_t)(chunk >> 4) * a.qs_group);
+      quant_group<16, VEC>(*reinterpret_cast<const float(*)[1][8]>(&v[i]), a.q, row * a.ld_q + col, n,
+                           a.q_scale + row * a.qs_row + (int64_t)(chunk >> 4) * a.qs_group);
   }
 }
 
 // Many rows: resident CTAs walk over the rows, and the next row's loads are in
 // flight while this row is summed and written.  Eight lanes hold a 128-column
-// group, two chunks of eight columns each: thread t's pair i stands in group
-// i * (threads / 8) + t / 8.  RW, DW: resid, delta in 32 bits.
-template <int PAIRS, int MAX_THREADS, bool RW, bool DW>
-__global__ void __launch_bounds__(MAX_THREADS, MAX_THREADS > 256 ? 1 : RW || DW ? 2 : 3) rmsnorm_rows_kernel(const ts_moe_rmsnorm_args a) {
+// group, two chunks of eight columns each: thread t's stand in group t / 8.
+// RW, DW: resid, delta in 32 bits.
+template <int MAX_THREADS, bool RW, bool DW>
+__global__ void __launch_bounds__(MAX_THREADS, MAX_THREADS > 256 ? 1024 / MAX_THREADS : RW || DW ? 2 : 3) rmsnorm_rows_kernel(const ts_moe_rmsnorm_args a) {
   __shared__ float warp_sum[2][MAX_THREADS / 32];
   grid_dep_wait();
   grid_dep_launch();
-  const int H = a.hidden, per = (int)blockDim.x / 8, g0 = (int)threadIdx.x / 8, lane_col = ((int)threadIdx.x & 7) * 8;
-  Raw<RW> nr[PAIRS][2];
-  Raw<DW> nd[PAIRS][2];
-  constexpr bool HOLD = PAIRS == 1;  // two pairs: registers go to the loads in flight, and gamma comes from L1
+  const int H = a.hidden, group = (int)threadIdx.x / 8, col0 = group * SCALE_BLOCK + ((int)threadIdx.x & 7) * 8;
+  Raw<RW> nr[2];
+  Raw<DW> nd[2];
+  constexpr bool HOLD = MAX_THREADS <= 256;  // else the registers go to the loads in flight, and gamma comes from L1
   Raw8 gg[2];
   auto fetch = [&](int64_t row) {
 #pragma unroll
-    for (int i = 0; i < PAIRS; ++i) {
-#pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        const int col = (g0 + i * per) * SCALE_BLOCK + lane_col + c * 64;
-        if (row < a.rows && col < H) {
-          nr[i][c] = load_vec<RW>(a.resid, row * a.ld_resid + col);
-          if (a.delta) nd[i][c] = load_vec<DW>(a.delta, row * a.ld_delta + col);
-        }
+    for (int c = 0; c < 2; ++c) {
+      const int col = col0 + c * 64;
+      if (row < a.rows && col < H) {
+        nr[c] = load_vec<RW>(a.resid, row * a.ld_resid + col);
+        if (a.delta) nd[c] = load_vec<DW>(a.delta, row * a.ld_delta + col);
       }
     }
   };
@@ -123,34 +121,31 @@ __global__ void __launch_bounds__(MAX_THREADS, MAX_THREADS > 256 ? 1 : RW || DW 
   if (HOLD && a.gamma) {
 #pragma unroll
     for (int c = 0; c < 2; ++c) {
-      const int col = g0 * SCALE_BLOCK + lane_col + c * 64;
+      const int col = col0 + c * 64;
       if (col < H) gg[c] = load_raw8<true>(a.gamma, a.gamma_type, col, 8);
     }
   }
   for (int buf = 0; row < a.rows; buf ^= 1) {
-    float v[PAIRS][2][8], ss = 0.f;
+    float v[2][8], ss = 0.f;
 #pragma unroll
-    for (int i = 0; i < PAIRS; ++i) {
+    for (int c = 0; c < 2; ++c) {
+      const int col = col0 + c * 64;
+      if (col < H) {
+        cvt_vec<RW>(nr[c], a.resid_type, v[c]);
+        if (a.delta) {
+          float d[8];
+          cvt_vec<DW>(nd[c], a.delta_type, d);
 #pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        const int col = (g0 + i * per) * SCALE_BLOCK + lane_col + c * 64;
-        if (col < H) {
-          cvt_vec<RW>(nr[i][c], a.resid_type, v[i][c]);
-          if (a.delta) {
-            float d[8];
-            cvt_vec<DW>(nd[i][c], a.delta_type, d);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) v[i][c][j] += d[j];
-            const Raw8 r = round8(v[i][c], RW ? TS_DT_FP32 : a.resid_type);
-            cvt8(r, RW ? TS_DT_FP32 : a.resid_type, v[i][c]);
-            if (a.resid_out) store_raw8<true>(a.resid_out, RW ? TS_DT_FP32 : a.resid_type, row * a.ld_resid_out + col, 8, r);
-          }
-#pragma unroll
-          for (int j = 0; j < 8; ++j) ss += v[i][c][j] * v[i][c][j];
-        } else {
-#pragma unroll
-          for (int j = 0; j < 8; ++j) v[i][c][j] = 0.f;
+          for (int j = 0; j < 8; ++j) v[c][j] += d[j];
+          const Raw8 r = round8(v[c], RW ? TS_DT_FP32 : a.resid_type);
+          cvt8(r, RW ? TS_DT_FP32 : a.resid_type, v[c]);
+          if (a.resid_out) store_raw8<true>(a.resid_out, RW ? TS_DT_FP32 : a.resid_type, row * a.ld_resid_out + col, 8, r);
         }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) ss += v[c][j] * v[c][j];
+      } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[c][j] = 0.f;
       }
     }
     const int64_t at = row;
@@ -158,25 +153,21 @@ __global__ void __launch_bounds__(MAX_THREADS, MAX_THREADS > 256 ? 1 : RW || DW 
     fetch(row);
     const float rstd = 1.f / sqrtf(norm_cta_sum(ss, warp_sum[buf]) / (float)H + a.eps);
 #pragma unroll
-    for (int i = 0; i < PAIRS; ++i) {
-      const int group = g0 + i * per, col0 = group * SCALE_BLOCK + lane_col;
+    for (int c = 0; c < 2; ++c) {
+      const int col = col0 + c * 64;
+      if (col < H) {
 #pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        const int col = col0 + c * 64;
-        if (col < H) {
+        for (int j = 0; j < 8; ++j) v[c][j] *= rstd;
+        if (a.gamma) {
+          float g[8];
+          cvt8(HOLD ? gg[c] : load_raw8<true>(a.gamma, a.gamma_type, col, 8), a.gamma_type, g);
 #pragma unroll
-          for (int j = 0; j < 8; ++j) v[i][c][j] *= rstd;
-          if (a.gamma) {
-            float g[8];
-            cvt8(HOLD ? gg[c] : load_raw8<true>(a.gamma, a.gamma_type, col, 8), a.gamma_type, g);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) v[i][c][j] *= g[j];
-          }
-          if (a.y) store_raw8<true>(a.y, a.y_type, at * a.ld_y + col, 8, round8(v[i][c], a.y_type));
+          for (int j = 0; j < 8; ++j) v[c][j] *= g[j];
         }
+        if (a.y) store_raw8<true>(a.y, a.y_type, at * a.ld_y + col, 8, round8(v[c], a.y_type));
       }
-      if (a.q) quant_group<8, true>(v[i], a.q, at * a.ld_q + col0, H - col0, a.q_scale + at * a.qs_row + (int64_t)group * a.qs_group);
     }
+    if (a.q) quant_group<8, true>(v, a.q, at * a.ld_q + col0, H - col0, a.q_scale + at * a.qs_row + (int64_t)group * a.qs_group);
   }
 }
 

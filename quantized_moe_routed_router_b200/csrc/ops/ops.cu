@@ -73,7 +73,8 @@ template <int BT>
 constexpr size_t stream_smem() {
   return sizeof(StreamSmem<BT>) + 1024;  // the struct starts at a 1024-byte boundary inside
 }
-constexpr size_t tile_smem() { return sizeof(TileSmem) + 1024; }
+constexpr size_t tile_smem() { return sizeof(TileSmem); }
+static_assert(tile_smem() <= 227 * 1024, "a CTA's shared memory");
 
 template <int BT>
 cudaError_t allow_stream() {
@@ -170,12 +171,12 @@ MatmulPlan matmul_plan(const ts_moe_fp8_matmul_args& a, int sms) {
 
 ts_moe_status done(cudaError_t e, const char* what) { return e == cudaSuccess ? TS_MOE_OK : cuda_bad(e, what); }
 
-template <int PAIRS, int MAX_THREADS>
+template <int MAX_THREADS>
 cudaError_t launch_norm_rows(const ts_moe_rmsnorm_args& a, void* stream) {
-  const int threads = cdiv(cdiv(cdiv(a.hidden, SCALE_BLOCK), PAIRS) * 8, 32) * 32;
+  const int threads = cdiv(cdiv(a.hidden, SCALE_BLOCK) * 8, 32) * 32;
   const bool rw = a.resid_type == TS_DT_FP32, dw = a.delta && a.delta_type == TS_DT_FP32;
-  auto k = rw ? (dw ? rmsnorm_rows_kernel<PAIRS, MAX_THREADS, true, true> : rmsnorm_rows_kernel<PAIRS, MAX_THREADS, true, false>)
-              : (dw ? rmsnorm_rows_kernel<PAIRS, MAX_THREADS, false, true> : rmsnorm_rows_kernel<PAIRS, MAX_THREADS, false, false>);
+  auto k = rw ? (dw ? rmsnorm_rows_kernel<MAX_THREADS, true, true> : rmsnorm_rows_kernel<MAX_THREADS, true, false>)
+              : (dw ? rmsnorm_rows_kernel<MAX_THREADS, false, true> : rmsnorm_rows_kernel<MAX_THREADS, false, false>);
   int per_sm = 1;
   const cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, k, threads, 0);
   if (e != cudaSuccess) return e;
@@ -185,9 +186,9 @@ cudaError_t launch_norm_rows(const ts_moe_rmsnorm_args& a, void* stream) {
 cudaError_t launch_norm(const ts_moe_rmsnorm_args& a, bool vec, void* stream) {
   const int chunks = cdiv(a.hidden, 8);
   if (vec && a.rows > 1024)
-    return a.hidden <= 4096   ? launch_norm_rows<1, 256>(a, stream)
-           : a.hidden <= 8192 ? launch_norm_rows<1, 512>(a, stream)
-                              : launch_norm_rows<2, 512>(a, stream);
+    return a.hidden <= 4096   ? launch_norm_rows<256>(a, stream)
+           : a.hidden <= 8192 ? launch_norm_rows<512>(a, stream)
+                              : launch_norm_rows<1024>(a, stream);
   const int it = a.rows <= 1024 ? (chunks <= 1024 ? 1 : 2) : 4;
   const int threads = std::max(32, cdiv(cdiv(chunks, it), 32) * 32);
   auto k = it == 1   ? (vec ? rmsnorm_kernel<1, true> : rmsnorm_kernel<1, false>)

@@ -43,6 +43,12 @@ TSM_DEV bool wait_cluster_or_die(uint64_t* bar, unsigned parity, volatile int* d
   }
 }
 
+// ----------------------------------------------------------------------------- registers of a warpgroup (all four warps call)
+template <int N>
+TSM_DEV void set_regs_down() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
+template <int N>
+TSM_DEV void set_regs_up() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
+
 // ----------------------------------------------------------------------------- cluster
 TSM_DEV uint32_t cluster_rank() {
   uint32_t r;
@@ -137,6 +143,31 @@ TSM_DEV void tmem_ld16(uint32_t addr, float (&v)[16]) {
   for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
 }
 
+// Thirty-two columns; tc_wait_ld32(v) before use.
+TSM_DEV void tmem_ld32(uint32_t addr, float (&v)[32]) {
+  uint32_t r[32];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(addr));
+#pragma unroll
+  for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+}
+TSM_DEV void tc_wait_ld32(float (&v)[32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]), "+f"(v[5]), "+f"(v[6]), "+f"(v[7]), "+f"(v[8]),
+                 "+f"(v[9]), "+f"(v[10]), "+f"(v[11]), "+f"(v[12]), "+f"(v[13]), "+f"(v[14]), "+f"(v[15]), "+f"(v[16]),
+                 "+f"(v[17]), "+f"(v[18]), "+f"(v[19]), "+f"(v[20]), "+f"(v[21]), "+f"(v[22]), "+f"(v[23]), "+f"(v[24]),
+                 "+f"(v[25]), "+f"(v[26]), "+f"(v[27]), "+f"(v[28])
+               :
+               : "memory");
+  asm volatile("" : "+f"(v[29]), "+f"(v[30]), "+f"(v[31]));
+}
+
 // Waits for this thread's loads from tensor memory.  Naming the registers keeps their uses behind it.
 TSM_DEV void tc_wait_ld(float (&v)[16]) {
   asm volatile("tcgen05.wait::ld.sync.aligned;"
@@ -144,6 +175,15 @@ TSM_DEV void tc_wait_ld(float (&v)[16]) {
                  "+f"(v[9]), "+f"(v[10]), "+f"(v[11]), "+f"(v[12]), "+f"(v[13]), "+f"(v[14]), "+f"(v[15])
                :
                : "memory");
+}
+
+// acc += s v on two values: one instruction for both.
+TSM_DEV void fma2(float2& acc, float s, float x, float y) {
+  unsigned long long d = *reinterpret_cast<unsigned long long*>(&acc);
+  asm("{\n\t.reg .b64 s2, v2;\n\tmov.b64 s2, {%1, %1};\n\tmov.b64 v2, {%2, %3};\n\tfma.rn.f32x2 %0, s2, v2, %0;\n\t}"
+      : "+l"(d)
+      : "f"(s), "f"(x), "f"(y));
+  acc = *reinterpret_cast<float2*>(&d);
 }
 
 }  // namespace tsm
