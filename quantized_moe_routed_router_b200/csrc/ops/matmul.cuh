@@ -101,19 +101,22 @@ TSM_DEV void store1(void* p, int type, int64_t i, float v) {
 }
 
 // ----------------------------------------------------------------------------- many rows
-constexpr int TL_M = 128, TL_N = 256, TL_STAGES = 4, TL_ACC = 2;  // TL_ACC x TL_N = all 512 columns of tensor memory
+constexpr int TL_M = 128, TL_N = 256, TL_STAGES = 3, TL_ACC = 2;  // TL_ACC x TL_N = all 512 columns of tensor memory
 constexpr int TL_BAND = 16;     // row tiles that run side by side over the columns: their rows of A stay in L2
-constexpr int TL_PARTS = 4, TL_COLS = TL_N / TL_PARTS;  // column parts of a tile: four warps scale and add one each
-constexpr int TL_ADDERS = 4 * TL_PARTS, TL_THREADS = 128 + 32 * TL_ADDERS;  // after the producer's and the MMAs' warpgroup
-// Registers a thread: at launch (what fits 640 threads), and as the two roles split them afterwards.
-constexpr int TL_REGS = 96, TL_REGS_ISSUE = 32, TL_REGS_ADD = 112;
+constexpr int TL_CHUNK = 4;     // scale blocks whose scales are staged at a time
+constexpr int TL_PITCH = 17;     // 16-byte places from row to row of the staged output: 16 and one that spreads rows over the banks
+constexpr int TL_PARTS = 2, TL_COLS = TL_N / TL_PARTS;  // column parts of a tile: four warps scale and add one each
+constexpr int TL_ADDERS = 4 * TL_PARTS, TL_THREADS = 128 + 32 * TL_ADDERS;  // after the producer, the MMA and two scale warps
+// Registers a thread: at launch (what fits 384 threads), and as the two roles split them afterwards.
+constexpr int TL_REGS = 168, TL_REGS_ISSUE = 56, TL_REGS_ADD = 224;
 static_assert(128 * TL_REGS_ISSUE + 32 * TL_ADDERS * TL_REGS_ADD <= TL_THREADS * TL_REGS, "the split fits the launch's registers");
 
 struct TileSmem {
   uint8_t a[TL_STAGES][TL_M * SCALE_BLOCK];
   uint8_t b[TL_STAGES][TL_N * SCALE_BLOCK];
-  uint4 out[TL_ADDERS][32 * 4];  // a warp's 32 rows of 64 bytes on their way out
-  uint64_t full[TL_STAGES], empty[TL_STAGES], acc_full[TL_ACC], acc_empty[TL_ACC], drain;
+  float scale[2][TL_CHUNK][TL_N / SCALE_BLOCK][TL_M];  // products of the scales, TL_CHUNK blocks at a time
+  uint4 out[TL_ADDERS][32 * TL_PITCH];  // a warp's 32 rows of 256 bytes on their way out
+  uint64_t full[TL_STAGES], empty[TL_STAGES], acc_full[TL_ACC], acc_empty[TL_ACC], sc_full[2], sc_empty[2], drain;
   uint32_t tmem;
   int dead;
   GroupTable groups;
@@ -145,82 +148,103 @@ TSM_DEV Tile locate_tile(const MatmulParams& p, const GroupTable& tab, int t) {
 }
 
 // Rows row0 .. row0 + 31 (below hi), columns col0 .. of one warp: lane l holds row row0 + l.  They go out through
-// `stage`, 64 bytes of each row at a time, so that a store covers whole sectors of few rows instead of 16 bytes of 32;
-// 16-byte places within a row are permuted by the row's number, which spreads them over the banks both ways.
-TSM_DEV int stage_at(int r, int c) { return r * 4 + (c ^ (r >> 1 & 3)); }
-
-TSM_DEV void store_tile(const ts_moe_fp8_matmul_args& a, const float2 (&acc)[TL_COLS / 2], uint4* stage, int row0, int hi, int col0) {
+// `stage`, 256 bytes of each row at a time.  Plain outputs at 16-byte places leave by bulk copies, each lane its own
+// row's, which run beside the next tile: all SMs reach their stores at about the same time, and stores by the threads
+// kept them from the next tile's sums until HBM had taken them.  The rest is stored by the threads, a row's columns
+// side by side.
+TSM_DEV void store_tile(const ts_moe_fp8_matmul_args& a, const float (&acc)[TL_COLS], uint4* stage, int row0, int hi, int col0) {
   const int lane = threadIdx.x & 31, type = a.out_type, es = dt_size(type), rows = min(32, hi - row0);
   if (rows <= 0 || col0 >= a.n) return;  // uniform in the warp
   const bool vec = ((uintptr_t)a.out | (uintptr_t)(a.ld_out * es)) % 16 == 0;
-  if (type != TS_DT_FP32 && !a.add && vec && col0 + TL_COLS <= a.n) {
+  uint4* mine = stage + lane * TL_PITCH;
+  if (type != TS_DT_FP32 && !a.add && vec && a.n % 8 == 0) {
+    bulk_wait_read();
 #pragma unroll
-    for (int h = 0; h < TL_COLS / 32; ++h) {
-#pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        const float2* v = &acc[h * 16 + c * 4];
-        stage[stage_at(lane, c)] = make_uint4(pack2(v[0].x, v[0].y, type), pack2(v[1].x, v[1].y, type), pack2(v[2].x, v[2].y, type),
-                                              pack2(v[3].x, v[3].y, type));
-      }
-      __syncwarp();
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int r = i * 8 + lane / 4, c = lane % 4;
-        if (r < rows) *(uint4*)((uint16_t*)a.out + (int64_t)(row0 + r) * a.ld_out + col0 + h * 32 + c * 8) = stage[stage_at(r, c)];
-      }
-      __syncwarp();
+    for (int c = 0; c < 16; ++c) {
+      const float* v = &acc[c * 8];
+      mine[c] = make_uint4(pack2(v[0], v[1], type), pack2(v[2], v[3], type), pack2(v[4], v[5], type), pack2(v[6], v[7], type));
     }
+    fence_proxy_async_smem();
+    if (lane < rows) bulk_s2g((uint16_t*)a.out + (int64_t)(row0 + lane) * a.ld_out + col0, mine, min(TL_COLS, a.n - col0) * 2);
+    bulk_commit();
     return;
   }
-  const bool vadd = ((uintptr_t)a.add | (uintptr_t)(a.ld_add * es)) % 16 == 0;
+  const bool vec4 = vec && a.n % 4 == 0 && ((uintptr_t)a.add | (uintptr_t)(a.ld_add * es)) % 16 == 0;
 #pragma unroll
-  for (int h = 0; h < TL_COLS / 16; ++h) {
+  for (int h = 0; h < TL_COLS / 64; ++h) {
+    const int c0 = col0 + h * 64, n = min(64, a.n - c0);
+    if (n <= 0) return;
+    bulk_wait_read();
 #pragma unroll
-    for (int c = 0; c < 4; ++c) {
-      const float2 x = acc[h * 8 + c * 2], y = acc[h * 8 + c * 2 + 1];
-      stage[stage_at(lane, c)] = make_uint4(__float_as_uint(x.x), __float_as_uint(x.y), __float_as_uint(y.x), __float_as_uint(y.y));
+    for (int c = 0; c < 16; ++c) {
+      const float* v = &acc[h * 64 + c * 4];
+      mine[c] = make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]));
+    }
+    if (type == TS_DT_FP32 && !a.add && vec4) {
+      fence_proxy_async_smem();
+      if (lane < rows) bulk_s2g((float*)a.out + (int64_t)(row0 + lane) * a.ld_out + c0, mine, n * 4);
+      bulk_commit();
+      continue;
     }
     __syncwarp();
-    const int c0 = col0 + h * 16;
-    if (vec && vadd && c0 + 16 <= a.n) {
+    if (vec4) {
+      const int half = lane / 16, place = lane % 16;
+      const int64_t col = c0 + place * 4;
+      if (place * 4 < n) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int r = i * 8 + lane / 4, c = lane % 4;
-        if (r < rows) {
-          const uint4 w = stage[stage_at(r, c)];
-          float v[4] = {__uint_as_float(w.x), __uint_as_float(w.y), __uint_as_float(w.z), __uint_as_float(w.w)};
-          const int64_t out = (int64_t)(row0 + r) * a.ld_out + c0 + c * 4, add = (int64_t)(row0 + r) * a.ld_add + c0 + c * 4;
-          if (type == TS_DT_FP32) {
-            if (a.add) {
-              const float4 d = *(const float4*)((const float*)a.add + add);
-              v[0] += d.x, v[1] += d.y, v[2] += d.z, v[3] += d.w;
-            }
-            *(float4*)((float*)a.out + out) = make_float4(v[0], v[1], v[2], v[3]);
-          } else {
-            if (a.add) {
-              const uint2 d = *(const uint2*)((const uint16_t*)a.add + add);
-              Raw8 raw;
-              raw.a = make_uint4(d.x, d.y, 0, 0);
-              float f[8];
-              cvt8(raw, type, f);
+        for (int r0 = 0; r0 < 32; r0 += 16) {
+          float d[8][4];
 #pragma unroll
-              for (int j = 0; j < 4; ++j) v[j] += f[j];
+          for (int i = 0; i < 8; ++i) {
+            const int r = r0 + i * 2 + half;
+            d[i][0] = d[i][1] = d[i][2] = d[i][3] = 0.f;
+            if (a.add && r < rows) {
+              const int64_t at = (int64_t)(row0 + r) * a.ld_add + col;
+              if (type == TS_DT_FP32) {
+                const float4 w = *(const float4*)((const float*)a.add + at);
+                d[i][0] = w.x, d[i][1] = w.y, d[i][2] = w.z, d[i][3] = w.w;
+              } else {
+                const uint2 w = *(const uint2*)((const uint16_t*)a.add + at);
+                Raw8 raw;
+                raw.a = make_uint4(w.x, w.y, 0, 0);
+                float f[8];
+                cvt8(raw, type, f);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) d[i][j] = f[j];
+              }
             }
-            *(uint2*)((uint16_t*)a.out + out) = make_uint2(pack2(v[0], v[1], type), pack2(v[2], v[3], type));
+          }
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const int r = r0 + i * 2 + half;
+            if (r < rows) {
+              const uint4 w = stage[r * TL_PITCH + place];
+              const float v[4] = {__uint_as_float(w.x) + d[i][0], __uint_as_float(w.y) + d[i][1], __uint_as_float(w.z) + d[i][2],
+                                  __uint_as_float(w.w) + d[i][3]};
+              const int64_t at = (int64_t)(row0 + r) * a.ld_out + col;
+              if (type == TS_DT_FP32)
+                *(float4*)((float*)a.out + at) = make_float4(v[0], v[1], v[2], v[3]);
+              else
+                *(uint2*)((uint16_t*)a.out + at) = make_uint2(pack2(v[0], v[1], type), pack2(v[2], v[3], type));
+            }
           }
         }
       }
     } else {
-      // odd places: sixteen columns of two rows at a time, element by element
+      // odd places: 32 columns of a row at a time, element by element
       const float* f = (const float*)stage;
-      const int c = lane % 16;
-#pragma unroll 4
-      for (int i = 0; i < 16; ++i) {
-        const int r = i * 2 + lane / 16;
-        if (r < rows && c0 + c < a.n) {
-          float v = f[stage_at(r, c / 4) * 4 + c % 4];
-          if (a.add) v += load1(a.add, type, (int64_t)(row0 + r) * a.ld_add + c0 + c);
-          store1(a.out, type, (int64_t)(row0 + r) * a.ld_out + c0 + c, v);
+#pragma unroll
+      for (int r0 = 0; r0 < 32; r0 += 8) {
+        float d[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const int r = r0 + i / 2, c = i % 2 * 32 + lane;
+          d[i] = a.add && r < rows && c < n ? load1(a.add, type, (int64_t)(row0 + r) * a.ld_add + c0 + c) : 0.f;
+        }
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const int r = r0 + i / 2, c = i % 2 * 32 + lane;
+          if (r < rows && c < n) store1(a.out, type, (int64_t)(row0 + r) * a.ld_out + c0 + c, f[r * TL_PITCH * 4 + c] + d[i]);
         }
       }
     }
@@ -239,6 +263,7 @@ __global__ void __launch_bounds__(TL_THREADS, 1)
   if (threadIdx.x == 0) {
     for (int i = 0; i < TL_STAGES; ++i) mbar_init(&s.full[i], 1), mbar_init(&s.empty[i], 1);
     for (int i = 0; i < TL_ACC; ++i) mbar_init(&s.acc_full[i], 1), mbar_init(&s.acc_empty[i], TL_ADDERS);
+    for (int i = 0; i < 2; ++i) mbar_init(&s.sc_full[i], 64), mbar_init(&s.sc_empty[i], TL_ADDERS);
     mbar_init(&s.drain, 1);
     s.dead = (smem_addr(raw) & 1023) != 0;
     fence_barrier_init();
@@ -279,76 +304,121 @@ __global__ void __launch_bounds__(TL_THREADS, 1)
       }
     }
   } else if (warp == 1) {
-    if (lane == 0) {
-      constexpr uint32_t idesc = umma_idesc(TL_M, TL_N);
-      unsigned it = 0;
-      for (int t = blockIdx.x; t < tiles && !*dead; t += gridDim.x) {
-        for (int c = 0; c < p.kb; ++c, ++it) {
-          const int st = it % TL_STAGES, ac = it % TL_ACC;
-          if (!wait_or_die(&s.acc_empty[ac], (it / TL_ACC & 1) ^ 1, dead)) break;
-          if (!wait_or_die(&s.full[st], it / TL_STAGES & 1, dead)) break;
-          tc_fence_after();
-          const uint64_t da = umma_desc(smem_addr(s.a[st])), db = umma_desc(smem_addr(s.b[st]));
+    // The whole warp runs the loop and one lane issues: descriptors computed where the warp is converged stay in uniform
+    // registers.  With the loop inside a branch of one lane a block's four MMAs and two commits took 550 cycles to issue
+    // and each wait 250, more than the 512 that the MMAs run.
+    constexpr uint32_t idesc = umma_idesc(TL_M, TL_N);
+    const uint64_t da0 = umma_desc(smem_addr(s.a[0])), db0 = umma_desc(smem_addr(s.b[0]));
+    unsigned it = 0;
+    for (int t = blockIdx.x; t < tiles && !*dead; t += gridDim.x) {
+      for (int c = 0; c < p.kb; ++c, ++it) {
+        const int st = it % TL_STAGES, ac = it % TL_ACC;
+        const bool ok = wait_both_or_die(&s.acc_empty[ac], (it / TL_ACC & 1) ^ 1, &s.full[st], it / TL_STAGES & 1, dead);
+        if (!__all_sync(0xFFFFFFFFu, ok)) break;
+        tc_fence_after();
+        const uint64_t da = da0 + st * (TL_M * SCALE_BLOCK / 16), db = db0 + st * (TL_N * SCALE_BLOCK / 16);
+        if (elect_one()) {
 #pragma unroll
           for (int k = 0; k < SCALE_BLOCK / 32; ++k) umma_e4m3(tmem + ac * TL_N, da + 2 * k, db + 2 * k, idesc, k > 0);
           umma_commit(&s.empty[st]);
           umma_commit(&s.acc_full[ac]);
         }
-      }
-      // no MMA may be in flight when tensor memory is freed
-      umma_commit(&s.drain);
-      const unsigned long long t0 = globaltimer();
-      while (!mbar_try_wait(&s.drain, 0) && globaltimer() - t0 < WAIT_LIMIT_NS) {
+        __syncwarp();
       }
     }
-  } else if (warp >= 4) {
+    // no MMA may be in flight when tensor memory is freed
+    if (elect_one()) umma_commit(&s.drain);
+    const unsigned long long t0 = globaltimer();
+    while (!mbar_try_wait(&s.drain, 0) && globaltimer() - t0 < WAIT_LIMIT_NS) {
+    }
+  } else if (warp < 4) {
+    // the scales: thread i those of the tile's rows i and i + 64, times the column blocks'
+    const int r = threadIdx.x - 64, nblocks = cdiv(p.a.n, SCALE_BLOCK);
+    const bool vec = p.a.as_block == 1 && ((uintptr_t)p.a.a_scale | (uintptr_t)(p.a.as_row * 4)) % 16 == 0;
+    unsigned it = 0;
+    for (int t = blockIdx.x; t < tiles && !*dead; t += gridDim.x) {
+      const Tile tl = locate_tile(p, s.groups, t);
+      const float* sb = p.a.b_scale + tl.g * p.a.bs_group;
+      const int64_t b0 = (int64_t)(tl.n0 / SCALE_BLOCK) * p.a.bs_row, b1 = (int64_t)min(tl.n0 / SCALE_BLOCK + 1, nblocks - 1) * p.a.bs_row;
+      for (int c0 = 0; c0 < p.kb; c0 += TL_CHUNK, ++it) {
+        if (!wait_or_die(&s.sc_empty[it & 1], (it / 2 & 1) ^ 1, dead)) break;
+        float(*out)[TL_N / SCALE_BLOCK][TL_M] = s.scale[it & 1];
+#pragma unroll 1
+        for (int h = 0; h < 2; ++h) {
+          const int row = r + h * 64;
+          const float* sa = p.a.a_scale + (int64_t)min(tl.m0 + row, tl.hi - 1) * p.a.as_row;
+          float v[TL_CHUNK];
+          if (vec && c0 + TL_CHUNK <= p.kb) {
+            const float4 w = *(const float4*)(sa + c0);
+            v[0] = w.x, v[1] = w.y, v[2] = w.z, v[3] = w.w;
+          } else {
+#pragma unroll
+            for (int i = 0; i < TL_CHUNK; ++i) v[i] = c0 + i < p.kb ? sa[(int64_t)(c0 + i) * p.a.as_block] : 0.f;
+          }
+#pragma unroll
+          for (int i = 0; i < TL_CHUNK; ++i) {
+            const int64_t c = (int64_t)min(c0 + i, p.kb - 1) * p.a.bs_block;
+            out[i][0][row] = v[i] * sb[b0 + c];
+            out[i][1][row] = v[i] * sb[b1 + c];
+          }
+        }
+        mbar_arrive(&s.sc_full[it & 1]);
+      }
+    }
+  } else {
     set_regs_up<TL_REGS_ADD>();
     const int quarter = warp & 3, part = (warp - 4) >> 2;
     const uint32_t mine = tmem + ((uint32_t)(quarter * 32) << 16) + part * TL_COLS;
-    const int nblocks = cdiv(p.a.n, SCALE_BLOCK);
-    unsigned it = 0;
+    const float* scale = &s.scale[0][0][part * TL_COLS / SCALE_BLOCK][quarter * 32 + lane];
+    unsigned it = 0, chunk = 0;
+    bool ready = false;
     for (int t = blockIdx.x; t < tiles; t += gridDim.x) {
-      const Tile tl = locate_tile(p, s.groups, t);
-      const int row0 = tl.m0 + quarter * 32, col0 = tl.n0 + part * TL_COLS;
-      const float* sa = p.a.a_scale + (int64_t)min(row0 + lane, tl.hi - 1) * p.a.as_row;
-      const float* sb = p.a.b_scale + tl.g * p.a.bs_group + (int64_t)min(col0 / SCALE_BLOCK, nblocks - 1) * p.a.bs_row;
-      float2 acc[TL_COLS / 2];
+      float acc[TL_COLS];
 #pragma unroll
-      for (int j = 0; j < TL_COLS / 2; ++j) acc[j] = make_float2(0.f, 0.f);
-      // the scales of two blocks ahead are on their way
-      float na = *sa, nb = *sb, ma2 = 0.f, mb2 = 0.f;
-      if (p.kb > 1) ma2 = sa[p.a.as_block], mb2 = sb[p.a.bs_block];
-      for (int c = 0; c < p.kb; ++c, ++it) {
-        const int ac = it % TL_ACC;
-        const float sc = na * nb;
-        na = ma2, nb = mb2;
-        if (c + 2 < p.kb) {
-          ma2 = sa[(int64_t)(c + 2) * p.a.as_block];
-          mb2 = sb[(int64_t)(c + 2) * p.a.bs_block];
-        }
-        wait_or_die(&s.acc_full[ac], it / TL_ACC & 1, dead);  // a dead CTA runs on without waiting
-        __syncwarp();
-        tc_fence_after();
+      for (int j = 0; j < TL_COLS; ++j) acc[j] = 0.f;
+      for (int c0 = 0; c0 < p.kb; c0 += TL_CHUNK, ++chunk) {
+        wait_or_die(&s.sc_full[chunk & 1], chunk / 2 & 1, dead);  // a dead CTA runs on without waiting
+        const float* from = scale + (chunk & 1) * (TL_CHUNK * (TL_N / SCALE_BLOCK) * TL_M);
+        const int ce = min(TL_CHUNK, p.kb - c0);
+        float next = *from;
+        for (int i = 0; i < ce; ++i, ++it) {
+          const int ac = it % TL_ACC;
+          const float sc = next;
+          if (!ready) wait_or_die(&s.acc_full[ac], it / TL_ACC & 1, dead);
+          __syncwarp();
+          tc_fence_after();
+          float v[2][32];
+          tmem_ld32(mine + ac * TL_N, v[0]);
+          // Shared memory answers after some 200 cycles beside the MMAs' and the copies' traffic: what the next block needs
+          // is asked for here.
+          if (i + 1 < ce) next = from[(i + 1) * (TL_N / SCALE_BLOCK * TL_M)];
 #pragma unroll
-        for (int q = 0; q < TL_COLS / 32; ++q) {
-          float v[32];
-          tmem_ld32(mine + ac * TL_N + q * 32, v);
-          tc_wait_ld32(v);
-          if (q == TL_COLS / 32 - 1) {  // all read: the MMAs may write here again
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&s.acc_empty[ac]);
+          for (int q = 0; q < TL_COLS / 32; ++q) {
+            tc_wait_ld(v[q & 1]);
+            if (q + 1 < TL_COLS / 32) {
+              tmem_ld32(mine + ac * TL_N + (q + 1) * 32, v[(q + 1) & 1]);
+            } else {  // all read: the MMAs may write here again
+              tc_fence_before();
+              __syncwarp();
+              if (lane == 0) {
+                mbar_arrive(&s.acc_empty[ac]);
+                if (i == ce - 1) mbar_arrive(&s.sc_empty[chunk & 1]);
+              }
+            }
+            if (q == 3) ready = mbar_test(&s.acc_full[(it + 1) % TL_ACC], (it + 1) / TL_ACC & 1);
+#pragma unroll
+            for (int j = 0; j < 32; ++j) acc[q * 32 + j] += sc * v[q & 1][j];
           }
-#pragma unroll
-          for (int j = 0; j < 16; ++j) fma2(acc[q * 16 + j], sc, v[2 * j], v[2 * j + 1]);
         }
       }
       if (*dead) {
 #pragma unroll
-        for (int j = 0; j < TL_COLS / 2; ++j) acc[j] = make_float2(NAN, NAN);
+        for (int j = 0; j < TL_COLS; ++j) acc[j] = NAN;
       }
-      store_tile(p.a, acc, s.out[warp - 4], row0, tl.hi, col0);
+      const Tile tl = locate_tile(p, s.groups, t);
+      store_tile(p.a, acc, s.out[warp - 4], tl.m0 + quarter * 32, tl.hi, tl.n0 + part * TL_COLS);
     }
+    bulk_wait();
   }
   __syncwarp();
   __syncthreads();

@@ -8,39 +8,71 @@
 namespace tsm {
 
 // ----------------------------------------------------------------------------- waits
-// Waits for the phase with `parity` of `bar`; gives up after WAIT_LIMIT_NS, or at
-// once when another thread of the CTA has, and marks the CTA dead.
-TSM_DEV bool wait_or_die(uint64_t* bar, unsigned parity, volatile int* dead) {
-  if (mbar_try_wait(bar, parity)) return true;
-  const unsigned long long t0 = globaltimer();
+// Waits for the phase with `parity` of `bar`; gives up after WAIT_LIMIT_NS, or when another thread of the CTA has,
+// and marks the CTA dead.  The clock and the mark are looked at once in WAIT_TRIES tries: both reads take longer than
+// a try, and a wait that ends meanwhile would be noticed late.  wait_cluster_or_die sees
+// what the cluster's other CTAs wrote before their arrivals.
+constexpr unsigned WAIT_TRIES = 64;
+
+TSM_DEV bool try_wait_cluster(uint64_t* bar, unsigned parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_addr(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+
+// Whether the phase has completed, without waiting.
+TSM_DEV bool mbar_test(uint64_t* bar, unsigned parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_addr(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+
+// `ready` tries once.
+template <typename Try>
+TSM_DEV bool bounded_wait(const Try& ready, volatile int* dead) {
+  unsigned long long t0 = 0;
   while (true) {
-    if (mbar_try_wait(bar, parity)) return true;
+    for (unsigned i = 0; i < WAIT_TRIES; ++i)
+      if (ready()) return true;
     if (*dead) return false;
-    if (globaltimer() - t0 > WAIT_LIMIT_NS) {
+    const unsigned long long now = globaltimer();
+    if (t0 == 0) t0 = now;
+    if (now - t0 > WAIT_LIMIT_NS) {
       *dead = 1;
       return false;
     }
   }
 }
-
-// The same, seeing what the cluster's other CTAs wrote before their arrivals.
+TSM_DEV bool wait_or_die(uint64_t* bar, unsigned parity, volatile int* dead) {
+  return bounded_wait([&] { return mbar_try_wait(bar, parity); }, dead);
+}
 TSM_DEV bool wait_cluster_or_die(uint64_t* bar, unsigned parity, volatile int* dead) {
-  const unsigned long long t0 = globaltimer();
-  while (true) {
-    uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok)
-        : "r"(smem_addr(bar)), "r"(parity)
-        : "memory");
-    if (ok) return true;
-    if (*dead) return false;
-    if (globaltimer() - t0 > WAIT_LIMIT_NS) {
-      *dead = 1;
-      return false;
-    }
-  }
+  return bounded_wait([&] { return try_wait_cluster(bar, parity); }, dead);
+}
+// Two barriers at once: the tries run side by side.
+TSM_DEV bool wait_both_or_die(uint64_t* a, unsigned pa, uint64_t* b, unsigned pb, volatile int* dead) {
+  return bounded_wait(
+      [&] {
+        const bool x = mbar_try_wait(a, pa), y = mbar_try_wait(b, pb);
+        return x && y;
+      },
+      dead);
+}
+
+// One lane of a converged warp, the same each time.
+TSM_DEV bool elect_one() {
+  uint32_t r;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+  return r != 0;
 }
 
 // ----------------------------------------------------------------------------- registers of a warpgroup (all four warps call)
@@ -90,6 +122,15 @@ TSM_DEV void tma_load_3d(void* dst, const CUtensorMap* m, int x, int y, int z, u
       "l"(m), "r"(x), "r"(y), "r"(z), "r"(smem_addr(bar))
       : "memory");
 }
+
+// ----------------------------------------------------------------------------- bulk stores
+// shared -> global, both addresses 16-byte aligned, a multiple of 16 bytes that this thread wrote and fenced.
+TSM_DEV void bulk_s2g(void* dst, const void* src, unsigned bytes) {
+  asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(smem_addr(src)), "r"(bytes) : "memory");
+}
+TSM_DEV void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
+TSM_DEV void bulk_wait_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }  // the sources may be written again
+TSM_DEV void bulk_wait() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
 
 // ----------------------------------------------------------------------------- tcgen05
 template <int COLS>
@@ -143,29 +184,16 @@ TSM_DEV void tmem_ld16(uint32_t addr, float (&v)[16]) {
   for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
 }
 
-// Thirty-two columns; tc_wait_ld32(v) before use.
+// Thirty-two columns; tc_wait_ld(v) before use.
 TSM_DEV void tmem_ld32(uint32_t addr, float (&v)[32]) {
-  uint32_t r[32];
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
       "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
-        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
-        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]), "=f"(v[8]),
+        "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15]), "=f"(v[16]),
+        "=f"(v[17]), "=f"(v[18]), "=f"(v[19]), "=f"(v[20]), "=f"(v[21]), "=f"(v[22]), "=f"(v[23]), "=f"(v[24]),
+        "=f"(v[25]), "=f"(v[26]), "=f"(v[27]), "=f"(v[28]), "=f"(v[29]), "=f"(v[30]), "=f"(v[31])
       : "r"(addr));
-#pragma unroll
-  for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
-}
-TSM_DEV void tc_wait_ld32(float (&v)[32]) {
-  asm volatile("tcgen05.wait::ld.sync.aligned;"
-               : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]), "+f"(v[5]), "+f"(v[6]), "+f"(v[7]), "+f"(v[8]),
-                 "+f"(v[9]), "+f"(v[10]), "+f"(v[11]), "+f"(v[12]), "+f"(v[13]), "+f"(v[14]), "+f"(v[15]), "+f"(v[16]),
-                 "+f"(v[17]), "+f"(v[18]), "+f"(v[19]), "+f"(v[20]), "+f"(v[21]), "+f"(v[22]), "+f"(v[23]), "+f"(v[24]),
-                 "+f"(v[25]), "+f"(v[26]), "+f"(v[27]), "+f"(v[28])
-               :
-               : "memory");
-  asm volatile("" : "+f"(v[29]), "+f"(v[30]), "+f"(v[31]));
 }
 
 // Waits for this thread's loads from tensor memory.  Naming the registers keeps their uses behind it.
@@ -176,14 +204,15 @@ TSM_DEV void tc_wait_ld(float (&v)[16]) {
                :
                : "memory");
 }
-
-// acc += s v on two values: one instruction for both.
-TSM_DEV void fma2(float2& acc, float s, float x, float y) {
-  unsigned long long d = *reinterpret_cast<unsigned long long*>(&acc);
-  asm("{\n\t.reg .b64 s2, v2;\n\tmov.b64 s2, {%1, %1};\n\tmov.b64 v2, {%2, %3};\n\tfma.rn.f32x2 %0, s2, v2, %0;\n\t}"
-      : "+l"(d)
-      : "f"(s), "f"(x), "f"(y));
-  acc = *reinterpret_cast<float2*>(&d);
+TSM_DEV void tc_wait_ld(float (&v)[32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]), "+f"(v[5]), "+f"(v[6]), "+f"(v[7]), "+f"(v[8]),
+                 "+f"(v[9]), "+f"(v[10]), "+f"(v[11]), "+f"(v[12]), "+f"(v[13]), "+f"(v[14]), "+f"(v[15]), "+f"(v[16]),
+                 "+f"(v[17]), "+f"(v[18]), "+f"(v[19]), "+f"(v[20]), "+f"(v[21]), "+f"(v[22]), "+f"(v[23]), "+f"(v[24]),
+                 "+f"(v[25]), "+f"(v[26]), "+f"(v[27]), "+f"(v[28]), "+f"(v[29])
+               :
+               : "memory");
+  asm volatile("" : "+f"(v[30]), "+f"(v[31]));
 }
 
 }  // namespace tsm
