@@ -22,6 +22,7 @@ struct MatmulParams {
   ts_moe_fp8_matmul_args a;
   int kb;      // scale blocks of K
   int splits;  // fp8_stream_kernel: CTAs of a cluster, which share K
+  int out_map; // fp8_tile_kernel: out has a tensor map (rows at 16-byte boundaries)
 };
 
 // ----------------------------------------------------------------------------- groups
@@ -104,7 +105,6 @@ TSM_DEV void store1(void* p, int type, int64_t i, float v) {
 constexpr int TL_M = 128, TL_N = 256, TL_STAGES = 3, TL_ACC = 2;  // TL_ACC x TL_N = all 512 columns of tensor memory
 constexpr int TL_BAND = 16;     // row tiles that run side by side over the columns: their rows of A stay in L2
 constexpr int TL_CHUNK = 4;     // scale blocks whose scales are staged at a time
-constexpr int TL_PITCH = 17;     // 16-byte places from row to row of the staged output: 16 and one that spreads rows over the banks
 constexpr int TL_PARTS = 2, TL_COLS = TL_N / TL_PARTS;  // column parts of a tile: four warps scale and add one each
 constexpr int TL_ADDERS = 4 * TL_PARTS, TL_THREADS = 128 + 32 * TL_ADDERS;  // after the producer, the MMA and two scale warps
 // Registers a thread: at launch (what fits 384 threads), and as the two roles split them afterwards.
@@ -114,8 +114,8 @@ static_assert(128 * TL_REGS_ISSUE + 32 * TL_ADDERS * TL_REGS_ADD <= TL_THREADS *
 struct TileSmem {
   uint8_t a[TL_STAGES][TL_M * SCALE_BLOCK];
   uint8_t b[TL_STAGES][TL_N * SCALE_BLOCK];
+  uint4 out[TL_ADDERS][2][32 * 8];  // a warp's 32 rows on their way out: two boxes of 128 bytes of each
   float scale[2][TL_CHUNK][TL_N / SCALE_BLOCK][TL_M];  // products of the scales, TL_CHUNK blocks at a time
-  uint4 out[TL_ADDERS][32 * TL_PITCH];  // a warp's 32 rows of 256 bytes on their way out
   uint64_t full[TL_STAGES], empty[TL_STAGES], acc_full[TL_ACC], acc_empty[TL_ACC], sc_full[2], sc_empty[2], drain;
   uint32_t tmem;
   int dead;
@@ -148,25 +148,76 @@ TSM_DEV Tile locate_tile(const MatmulParams& p, const GroupTable& tab, int t) {
 }
 
 // Rows row0 .. row0 + 31 (below hi), columns col0 .. of one warp: lane l holds row row0 + l.  They go out through
-// `stage`, 256 bytes of each row at a time.  Plain outputs at 16-byte places leave by bulk copies, each lane its own
-// row's, which run beside the next tile: all SMs reach their stores at about the same time, and stores by the threads
-// kept them from the next tile's sums until HBM had taken them.  The rest is stored by the threads, a row's columns
-// side by side.
-TSM_DEV void store_tile(const ts_moe_fp8_matmul_args& a, const float (&acc)[TL_COLS], uint4* stage, int row0, int hi, int col0) {
+// `stage`: two boxes of 128 bytes of each row at a time, 16-byte place c of row r at c ^ (r & 7) (the 128-byte swizzle,
+// which also spreads rows over the banks).  Plain outputs leave by tensor-map stores, which run beside the next tile:
+// all SMs reach their stores at about the same time, and stores by the threads kept them from the next tile's sums
+// until HBM had taken them.  Odd places and a group's last rows are stored by the threads, and so are sums with `add`.
+TSM_DEV int stage_at(int r, int c) { return c / 8 * 256 + r * 8 + (c % 8 ^ (r & 7)); }
+
+// Rows of `bytes` bytes (at most 256) from the stage to dst, ld bytes apart, at any places that elements of 2 or 4 bytes
+// can have: each lane shifts two 16-byte places into the 16 bytes that stand at a boundary in memory.  Stores of single
+// elements are kept to the rows' ends: sectors written in parts are several times as dear.
+TSM_DEV void flush_rows(const uint4* stage, char* dst, int64_t ld, int bytes, int rows) {
+  const int lane = threadIdx.x & 31, half = lane / 16, j = lane % 16;
+#pragma unroll 2
+  for (int r = half; r < rows; r += 2) {
+    char* row = dst + r * ld;
+    const int shift = (int)((uintptr_t)row & 15), at = 16 * j - shift;
+    const uint4 hi = stage[stage_at(r, j)], lo = j > 0 ? stage[stage_at(r, j - 1)] : make_uint4(0, 0, 0, 0);
+    uint32_t w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+    const int skip = 16 - shift;  // bytes of lo and hi before the ones wanted
+    if (skip & 16) w[0] = w[4], w[1] = w[5], w[2] = w[6], w[3] = w[7];
+    if (skip & 8) w[0] = w[2], w[1] = w[3], w[2] = w[4], w[3] = w[5], w[4] = w[6], w[5] = w[7];
+    if (skip & 4) w[0] = w[1], w[1] = w[2], w[2] = w[3], w[3] = w[4], w[4] = w[5];
+    uint32_t v[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = skip & 2 ? __funnelshift_r(w[i], w[i + 1], 16) : w[i];
+    if (at >= 0 && at + 16 <= bytes) {
+      *(uint4*)(row + at) = make_uint4(v[0], v[1], v[2], v[3]);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        if (at + 2 * e >= 0 && at + 2 * e < bytes) *(uint16_t*)(row + at + 2 * e) = (uint16_t)(v[e / 2] >> (16 * (e % 2)));
+    }
+  }
+  // what shifts past the sixteenth place
+  if (lane < rows) {
+    char* row = dst + lane * ld;
+    const int shift = (int)((uintptr_t)row & 15);
+    if (256 - shift < bytes) {
+      const uint4 last = stage[stage_at(lane, 15)];
+      const uint32_t v[4] = {last.x, last.y, last.z, last.w};
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        if (2 * e >= 16 - shift && 240 + 2 * e < bytes) *(uint16_t*)(row + 240 + 2 * e) = (uint16_t)(v[e / 2] >> (16 * (e % 2)));
+    }
+  }
+}
+
+TSM_DEV void store_tile(const MatmulParams& p, const CUtensorMap* mo, const float (&acc)[TL_COLS], uint4* stage, int row0, int hi, int col0) {
+  const ts_moe_fp8_matmul_args& a = p.a;
   const int lane = threadIdx.x & 31, type = a.out_type, es = dt_size(type), rows = min(32, hi - row0);
   if (rows <= 0 || col0 >= a.n) return;  // uniform in the warp
   const bool vec = ((uintptr_t)a.out | (uintptr_t)(a.ld_out * es)) % 16 == 0;
-  uint4* mine = stage + lane * TL_PITCH;
-  if (type != TS_DT_FP32 && !a.add && vec && a.n % 8 == 0) {
-    bulk_wait_read();
+  const bool mapped = p.out_map && !a.add && (rows == 32 || hi == a.rows);  // the map ends at row a.rows
+  char* const out0 = (char*)a.out + ((int64_t)row0 * a.ld_out + col0) * es;
+  if (type != TS_DT_FP32 && !a.add) {
+    if (lane == 0) bulk_wait_read();
+    __syncwarp();
 #pragma unroll
     for (int c = 0; c < 16; ++c) {
       const float* v = &acc[c * 8];
-      mine[c] = make_uint4(pack2(v[0], v[1], type), pack2(v[2], v[3], type), pack2(v[4], v[5], type), pack2(v[6], v[7], type));
+      stage[stage_at(lane, c)] = make_uint4(pack2(v[0], v[1], type), pack2(v[2], v[3], type), pack2(v[4], v[5], type), pack2(v[6], v[7], type));
     }
-    fence_proxy_async_smem();
-    if (lane < rows) bulk_s2g((uint16_t*)a.out + (int64_t)(row0 + lane) * a.ld_out + col0, mine, min(TL_COLS, a.n - col0) * 2);
-    bulk_commit();
+    if (mapped) fence_proxy_async_smem();
+    __syncwarp();
+    if (!mapped) {
+      flush_rows(stage, out0, a.ld_out * 2, min(TL_COLS, a.n - col0) * 2, rows);
+    } else if (lane == 0) {
+      tma_store_2d(mo, col0, row0, stage);
+      if (col0 + 64 < a.n) tma_store_2d(mo, col0 + 64, row0, stage + 256);
+      bulk_commit();
+    }
     return;
   }
   const bool vec4 = vec && a.n % 4 == 0 && ((uintptr_t)a.add | (uintptr_t)(a.ld_add * es)) % 16 == 0;
@@ -174,20 +225,27 @@ TSM_DEV void store_tile(const ts_moe_fp8_matmul_args& a, const float (&acc)[TL_C
   for (int h = 0; h < TL_COLS / 64; ++h) {
     const int c0 = col0 + h * 64, n = min(64, a.n - c0);
     if (n <= 0) return;
-    bulk_wait_read();
+    if (lane == 0) bulk_wait_read();
+    __syncwarp();
 #pragma unroll
     for (int c = 0; c < 16; ++c) {
       const float* v = &acc[h * 64 + c * 4];
-      mine[c] = make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]));
+      stage[stage_at(lane, c)] = make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]));
     }
-    if (type == TS_DT_FP32 && !a.add && vec4) {
+    if (type == TS_DT_FP32 && mapped) {
       fence_proxy_async_smem();
-      if (lane < rows) bulk_s2g((float*)a.out + (int64_t)(row0 + lane) * a.ld_out + c0, mine, n * 4);
-      bulk_commit();
+      __syncwarp();
+      if (lane == 0) {
+        tma_store_2d(mo, c0, row0, stage);
+        if (n > 32) tma_store_2d(mo, c0 + 32, row0, stage + 256);
+        bulk_commit();
+      }
       continue;
     }
     __syncwarp();
-    if (vec4) {
+    if (!a.add) {
+      flush_rows(stage, out0 + h * 256, a.ld_out * 4, n * 4, rows);
+    } else if (vec4) {
       const int half = lane / 16, place = lane % 16;
       const int64_t col = c0 + place * 4;
       if (place * 4 < n) {
@@ -198,7 +256,7 @@ TSM_DEV void store_tile(const ts_moe_fp8_matmul_args& a, const float (&acc)[TL_C
           for (int i = 0; i < 8; ++i) {
             const int r = r0 + i * 2 + half;
             d[i][0] = d[i][1] = d[i][2] = d[i][3] = 0.f;
-            if (a.add && r < rows) {
+            if (r < rows) {
               const int64_t at = (int64_t)(row0 + r) * a.ld_add + col;
               if (type == TS_DT_FP32) {
                 const float4 w = *(const float4*)((const float*)a.add + at);
@@ -218,7 +276,7 @@ TSM_DEV void store_tile(const ts_moe_fp8_matmul_args& a, const float (&acc)[TL_C
           for (int i = 0; i < 8; ++i) {
             const int r = r0 + i * 2 + half;
             if (r < rows) {
-              const uint4 w = stage[r * TL_PITCH + place];
+              const uint4 w = stage[stage_at(r, place)];
               const float v[4] = {__uint_as_float(w.x) + d[i][0], __uint_as_float(w.y) + d[i][1], __uint_as_float(w.z) + d[i][2],
                                   __uint_as_float(w.w) + d[i][3]};
               const int64_t at = (int64_t)(row0 + r) * a.ld_out + col;
@@ -239,12 +297,12 @@ TSM_DEV void store_tile(const ts_moe_fp8_matmul_args& a, const float (&acc)[TL_C
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
           const int r = r0 + i / 2, c = i % 2 * 32 + lane;
-          d[i] = a.add && r < rows && c < n ? load1(a.add, type, (int64_t)(row0 + r) * a.ld_add + c0 + c) : 0.f;
+          d[i] = r < rows && c < n ? load1(a.add, type, (int64_t)(row0 + r) * a.ld_add + c0 + c) : 0.f;
         }
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
           const int r = r0 + i / 2, c = i % 2 * 32 + lane;
-          if (r < rows && c < n) store1(a.out, type, (int64_t)(row0 + r) * a.ld_out + c0 + c, f[r * TL_PITCH * 4 + c] + d[i]);
+          if (r < rows && c < n) store1(a.out, type, (int64_t)(row0 + r) * a.ld_out + c0 + c, f[stage_at(r, c / 4) * 4 + c % 4] + d[i]);
         }
       }
     }
@@ -253,7 +311,8 @@ TSM_DEV void store_tile(const ts_moe_fp8_matmul_args& a, const float (&acc)[TL_C
 }
 
 __global__ void __launch_bounds__(TL_THREADS, 1)
-    fp8_tile_kernel(const MatmulParams p, const __grid_constant__ CUtensorMap ma, const __grid_constant__ CUtensorMap mb) {
+    fp8_tile_kernel(const __grid_constant__ MatmulParams p, const __grid_constant__ CUtensorMap ma,
+                    const __grid_constant__ CUtensorMap mb, const __grid_constant__ CUtensorMap mo) {
   // Without static shared memory the dynamic part starts at a 1024-byte boundary, as the swizzled tiles need it; were it
   // otherwise, the CTA would be dead from the start and its outputs NaN.
   extern __shared__ uint8_t raw[];
@@ -416,9 +475,9 @@ __global__ void __launch_bounds__(TL_THREADS, 1)
         for (int j = 0; j < TL_COLS; ++j) acc[j] = NAN;
       }
       const Tile tl = locate_tile(p, s.groups, t);
-      store_tile(p.a, acc, s.out[warp - 4], tl.m0 + quarter * 32, tl.hi, tl.n0 + part * TL_COLS);
+      store_tile(p, &mo, acc, s.out[warp - 4][0], tl.m0 + quarter * 32, tl.hi, tl.n0 + part * TL_COLS);
     }
-    bulk_wait();
+    if (lane == 0) bulk_wait();
   }
   __syncwarp();
   __syncthreads();

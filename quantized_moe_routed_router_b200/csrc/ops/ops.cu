@@ -123,6 +123,18 @@ bool encode_rows(CUtensorMap* m, const uint8_t* p, int k, int rows, int64_t ld, 
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// Map of out for stores of 32 rows x 128 bytes; rows start at 16-byte boundaries.
+bool encode_out(CUtensorMap* m, const ts_moe_fp8_matmul_args& a) {
+  const int es = dt_size(a.out_type);
+  cuuint64_t dims[2] = {(cuuint64_t)a.n, (cuuint64_t)a.rows}, strides[1] = {(cuuint64_t)a.ld_out * es};
+  cuuint32_t box[2] = {(cuuint32_t)(128 / es), 32}, one[2] = {1, 1};
+  const CUtensorMapDataType type = a.out_type == TS_DT_FP32   ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
+                                   : a.out_type == TS_DT_FP16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
+                                                              : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+  return g_encode(m, type, 2, a.out, dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                  CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 template <int BT>
 cudaError_t launch_stream(const MatmulParams& p, const CUtensorMap& ma, const CUtensorMap& mb, int clusters, void* stream) {
   return launch_clusters(fp8_stream_kernel<BT>, dim3(clusters * p.splits), ST_THREADS, stream_smem<BT>(), stream, p.splits, p, ma, mb);
@@ -283,9 +295,12 @@ ts_moe_status ts_moe_fp8_matmul(const ts_moe_fp8_matmul_args* args, void* stream
   CUtensorMap ma, mb;
   if (!encode_rows(&ma, a.a, a.k, a.rows, ld_a, -1, 0, plan.box_a) || !encode_rows(&mb, a.b, a.k, a.n, ld_b, a.num_groups, group, plan.box_b))
     return set_last_error(TS_MOE_ECUDA, "fp8_matmul: the driver refused a tensor map");
+  CUtensorMap mo = {};
+  p.out_map = plan.bt == 0 && !a.add && aligned(a.out, a.ld_out * dt_size(a.out_type), 16) && a.ld_out < (int64_t)1 << 37;
+  if (p.out_map && !encode_out(&mo, a)) return set_last_error(TS_MOE_ECUDA, "fp8_matmul: the driver refused a tensor map");
   cudaError_t e;
   if (plan.bt == 0)
-    e = launch(fp8_tile_kernel, dim3(plan.grid), TL_THREADS, tile_smem(), stream, p, ma, mb);
+    e = launch(fp8_tile_kernel, dim3(plan.grid), TL_THREADS, tile_smem(), stream, p, ma, mb, mo);
   else if (plan.bt == 16)
     e = launch_stream<16>(p, ma, mb, plan.grid, stream);
   else if (plan.bt == 32)

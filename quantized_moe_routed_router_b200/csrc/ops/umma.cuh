@@ -123,10 +123,12 @@ TSM_DEV void tma_load_3d(void* dst, const CUtensorMap* m, int x, int y, int z, u
       : "memory");
 }
 
-// ----------------------------------------------------------------------------- bulk stores
-// shared -> global, both addresses 16-byte aligned, a multiple of 16 bytes that this thread wrote and fenced.
-TSM_DEV void bulk_s2g(void* dst, const void* src, unsigned bytes) {
-  asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(smem_addr(src)), "r"(bytes) : "memory");
+// ----------------------------------------------------------------------------- tensor-map stores
+// Stores a tile of shared memory that this thread fenced; what lies past the map's extents is left out.
+TSM_DEV void tma_store_2d(const CUtensorMap* m, int x, int y, const void* src) {
+  asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%1, %2}], [%3];" ::"l"(m), "r"(x), "r"(y),
+               "r"(smem_addr(src))
+               : "memory");
 }
 TSM_DEV void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
 TSM_DEV void bulk_wait_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }  // the sources may be written again
