@@ -95,8 +95,6 @@ ts_moe_status matmul_setup(const MatmulDevice** out) {
     if (e == cudaSuccess) e = cudaFuncSetAttribute(fp8_tile_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)tile_smem());
     if (e == cudaSuccess) e = allow_stream<16>();
     if (e == cudaSuccess) e = allow_stream<32>();
-    if (e == cudaSuccess) e = allow_stream<64>();
-    if (e == cudaSuccess) e = allow_stream<128>();
     if (e != cudaSuccess) return cuda_bad(e, "fp8_matmul set-up");
     if (!g_encode) {
       void* fn = nullptr;
@@ -142,43 +140,40 @@ cudaError_t launch_stream(const MatmulParams& p, const CUtensorMap& ma, const CU
 
 // Which kernel, and how its work is cut.
 struct MatmulPlan {
-  int bt;      // rows of an fp8_stream_kernel tile; 0: fp8_tile_kernel
+  enum Kind { ROWS, STREAM, TILE } kind;
+  int bt;      // rows of an fp8_stream_kernel tile
   int splits;  // CTAs that share K
-  int grid;    // CTAs (tile kernel) or clusters
-  int box_a, box_b;
+  int grid;    // CTAs, or clusters
 };
 
+// The times below are microseconds, of calls one after another.
 MatmulPlan matmul_plan(const ts_moe_fp8_matmul_args& a, int sms) {
   const int kb = cdiv(a.k, SCALE_BLOCK), G = a.num_groups;
-  const int64_t reached = std::min(G, a.rows);            // groups that can hold a row
+  const int64_t reached = std::min(G, a.rows);  // groups that can hold a row
   const int64_t mean = cdiv(a.rows, (int)reached);
   const int64_t tiles = (cdiv(a.rows, TL_M) + reached - 1) * cdiv(a.n, TL_N);
-  MatmulPlan p;
-  if (mean > 128 && tiles >= sms) {
-    p.bt = 0;
-    p.splits = 1;
-    p.grid = (int)std::min<int64_t>(tiles, sms);
-    p.box_a = TL_M;
-    p.box_b = TL_N;
-    return p;
-  }
-  p.bt = G > 1 ? (mean <= 4 ? 16 : mean <= 12 ? 32 : mean <= 32 ? 64 : 128) : (mean <= 16 ? 16 : mean <= 32 ? 32 : mean <= 64 ? 64 : 128);
-  const int64_t items = (cdiv(a.rows, p.bt) + reached - 1) * cdiv(a.n, ST_N);
-  // the number of CTAs per tile that leaves the busiest SM the fewest blocks of K
-  const int per_sm = p.bt == 128 ? 1 : 2;
-  int64_t best = -1;
-  p.splits = 1;
-  for (int s = 1; s <= std::min(8, kb); ++s) {
-    const int64_t cost = cdiv((int)std::min<int64_t>(items * s, 1 << 30), sms) * (int64_t)cdiv(kb, s);
-    if (best < 0 || cost < best) {
-      best = cost;
-      p.splits = s;
-    }
-  }
-  p.grid = (int)std::min<int64_t>(items, std::max(1, sms * per_sm / p.splits));
-  p.box_a = p.bt;
-  p.box_b = ST_N;
-  return p;
+  const MatmulPlan tile = {MatmulPlan::TILE, 0, 1, (int)std::min<int64_t>(tiles, sms)};
+  // 1 x 4096 x 4096 6.2 against 8.9 by fp8_stream_kernel; with a second group of eight rows 10.4 against 9.0 (16 x 5760 x 2880)
+  if (!a.offsets && a.rows <= RW_MAX_ROWS) return {MatmulPlan::ROWS, 0, 1, cdiv(a.n, RW_N)};
+  // Groups: the sizes are not known here.  Up to 16 rows a group on average the narrow tiles read the matrices faster
+  // (32 groups of 5760 x 2880: 64 rows 72.6 against 79.4, 256 rows 85.5 against 94.0); beyond, groups take more tiles than
+  // one (1024 rows 114 against 103; 64 groups of 2816 x 2048, 2048 rows 84 against 71).
+  if (G > 1 && mean > 16) return tile;
+  const int bt = mean <= 16 ? 16 : 32;
+  const int64_t items = (cdiv(a.rows, bt) + reached - 1) * cdiv(a.n, ST_N);
+  // K is split while that leaves one CTA an SM, or two where one would leave K whole, never into a second wave: a cluster
+  // joins its shares in some 1 to 2 us (64 x 4096 x 4096: whole 14.8, 2 ways 11.5, 4 ways 11.4, 8 ways 25.0).
+  const int splits = (int)std::max<int64_t>(1, std::min<int64_t>(std::min(4, kb), (items * 2 <= sms ? sms : 2 * sms) / items));
+  const MatmulPlan stream = {MatmulPlan::STREAM, bt, splits, (int)std::min<int64_t>(items, 2 * sms / splits)};
+  if (G > 1) return stream;
+  // One matrix: what each would take, by 0.5 a block of K and tile against a fixed 7.5 and the larger of 0.13 a block in
+  // sequence and the traffic from L2 at 8 TB/s (128 x 4096 x 4096: 20.1 against 13.6; 128 x 14336 x 4096: 22.7 against 36.7).
+  // Tiles wait for what they add, and shift rows at odd places (333 x 2047 x 1408: 10.4 plain, 13.1 odd, 24.2 odd with add).
+  const double rest = (a.add ? 5.0 : 0.0) + (aligned(a.out, a.ld_out * dt_size(a.out_type), 16) ? 0.0 : 3.0);
+  const double t_tile = 4.0 + (double)((tiles + sms - 1) / sms) * (1.5 + 0.5 * kb + rest);
+  const double t_stream = 7.5 + std::max(0.13 * (double)((items * splits + 2 * sms - 1) / (2 * sms)) * cdiv(kb, splits),
+                                         (double)items * kb * (SCALE_BLOCK * (ST_N + bt)) / 8e6);
+  return t_tile <= t_stream ? tile : stream;
 }
 
 ts_moe_status done(cudaError_t e, const char* what) { return e == cudaSuccess ? TS_MOE_OK : cuda_bad(e, what); }
@@ -292,23 +287,22 @@ ts_moe_status ts_moe_fp8_matmul(const ts_moe_fp8_matmul_args* args, void* stream
   // strides no row or matrix follows may be anything: give the map valid ones
   const int64_t row = (a.k + 15) / 16 * 16, ld_a = a.rows > 1 ? a.ld_a : row, ld_b = a.n > 1 ? a.ld_b : row;
   const int64_t group = a.num_groups > 1 ? a.b_group : (int64_t)a.n * ld_b;
-  CUtensorMap ma, mb;
-  if (!encode_rows(&ma, a.a, a.k, a.rows, ld_a, -1, 0, plan.box_a) || !encode_rows(&mb, a.b, a.k, a.n, ld_b, a.num_groups, group, plan.box_b))
-    return set_last_error(TS_MOE_ECUDA, "fp8_matmul: the driver refused a tensor map");
-  CUtensorMap mo = {};
-  p.out_map = plan.bt == 0 && !a.add && aligned(a.out, a.ld_out * dt_size(a.out_type), 16) && a.ld_out < (int64_t)1 << 37;
-  if (p.out_map && !encode_out(&mo, a)) return set_last_error(TS_MOE_ECUDA, "fp8_matmul: the driver refused a tensor map");
   cudaError_t e;
-  if (plan.bt == 0)
+  if (plan.kind == MatmulPlan::ROWS) {
+    p.out_map = 0;
+    e = launch(fp8_row_kernel, dim3(plan.grid), RW_THREADS, 0, stream, p);
+    return done(e, "fp8_matmul launch");
+  }
+  const bool tile = plan.kind == MatmulPlan::TILE;
+  CUtensorMap ma, mb, mo = {};
+  p.out_map = tile && aligned(a.out, a.ld_out * dt_size(a.out_type), 16) && a.ld_out < (int64_t)1 << 37;
+  if (!encode_rows(&ma, a.a, a.k, a.rows, ld_a, -1, 0, tile ? TL_M : plan.bt) ||
+      !encode_rows(&mb, a.b, a.k, a.n, ld_b, a.num_groups, group, tile ? TL_N : ST_N) || (p.out_map && !encode_out(&mo, a)))
+    return set_last_error(TS_MOE_ECUDA, "fp8_matmul: the driver refused a tensor map");
+  if (tile)
     e = launch(fp8_tile_kernel, dim3(plan.grid), TL_THREADS, tile_smem(), stream, p, ma, mb, mo);
-  else if (plan.bt == 16)
-    e = launch_stream<16>(p, ma, mb, plan.grid, stream);
-  else if (plan.bt == 32)
-    e = launch_stream<32>(p, ma, mb, plan.grid, stream);
-  else if (plan.bt == 64)
-    e = launch_stream<64>(p, ma, mb, plan.grid, stream);
   else
-    e = launch_stream<128>(p, ma, mb, plan.grid, stream);
+    e = plan.bt == 16 ? launch_stream<16>(p, ma, mb, plan.grid, stream) : launch_stream<32>(p, ma, mb, plan.grid, stream);
   return done(e, "fp8_matmul launch");
 }
 

@@ -134,6 +134,16 @@ TSM_DEV void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "mem
 TSM_DEV void bulk_wait_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }  // the sources may be written again
 TSM_DEV void bulk_wait() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
 
+// ----------------------------------------------------------------------------- element copies
+// global -> shared without registers: 16 bytes at 16-byte places, of which `bytes` are read and the rest zeros; 4 bytes.
+TSM_DEV void copy16_async(void* dst, const void* src, int bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_addr(dst)), "l"(src), "r"(bytes) : "memory");
+}
+TSM_DEV void copy4_async(void* dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_addr(dst)), "l"(src) : "memory");
+}
+TSM_DEV void copy_wait() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+
 // ----------------------------------------------------------------------------- tcgen05
 template <int COLS>
 TSM_DEV void tmem_alloc(uint32_t* slot) {  // one whole warp
@@ -175,7 +185,7 @@ TSM_DEV void umma_commit(uint64_t* bar) {
 }
 
 // Sixteen columns of this warp's 32 lanes (lane quarter warp % 4); tc_wait_ld(v) before use.
-TSM_DEV void tmem_ld16(uint32_t addr, float (&v)[16]) {
+TSM_DEV void tmem_ld(uint32_t addr, float (&v)[16]) {
   uint32_t r[16];
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
@@ -186,8 +196,8 @@ TSM_DEV void tmem_ld16(uint32_t addr, float (&v)[16]) {
   for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
 }
 
-// Thirty-two columns; tc_wait_ld(v) before use.
-TSM_DEV void tmem_ld32(uint32_t addr, float (&v)[32]) {
+// Thirty-two columns.
+TSM_DEV void tmem_ld(uint32_t addr, float (&v)[32]) {
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
       "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
