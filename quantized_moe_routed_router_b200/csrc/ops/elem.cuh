@@ -171,10 +171,16 @@ TSM_DEV float rcp(float x) {
   return r;
 }
 
-// Maximum that keeps a NaN (fmaxf drops it).
+// Maximum and minimum that keep a NaN (fmaxf and fminf drop it).
 TSM_DEV float max_nan(float a, float b) {
   float r;
   asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+
+TSM_DEV float min_nan(float a, float b) {
+  float r;
+  asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
   return r;
 }
 

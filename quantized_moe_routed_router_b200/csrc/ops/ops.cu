@@ -204,6 +204,17 @@ cudaError_t launch_norm(const ts_moe_rmsnorm_args& a, bool vec, void* stream) {
   return launch(k, dim3(a.rows), threads, 0, stream, a);
 }
 
+template <bool SIGMOID, bool WIDE>
+void (*balance_instance(int experts))(const BalanceParams) {
+  const int lanes = balance_lanes(experts);
+  return lanes == 2     ? balance_kernel<2, 1, SIGMOID, WIDE>
+         : lanes == 4   ? balance_kernel<4, 1, SIGMOID, WIDE>
+         : lanes == 8   ? balance_kernel<8, 1, SIGMOID, WIDE>
+         : lanes == 16  ? balance_kernel<16, 1, SIGMOID, WIDE>
+         : experts <= 128 ? balance_kernel<32, 1, SIGMOID, WIDE>
+                        : balance_kernel<32, 2, SIGMOID, WIDE>;
+}
+
 }  // namespace
 
 extern "C" {
@@ -339,25 +350,17 @@ ts_moe_status ts_moe_balance(const ts_moe_balance_args* args, void* stream) {
   p.a = a;
   p.head = (BalanceHead*)a.workspace;
   p.part = (float*)((char*)a.workspace + sizeof(BalanceHead));
-  const int lanes = balance_lanes(a.experts);
   const int ctas = balance_ctas(a.rows, a.experts);
-  p.counted = ctas > 1 && a.dlogits ? 1 : 0;
-  if (ctas > 1) {
-    const cudaError_t e = cudaMemsetAsync(p.head, 0, sizeof(BalanceHead), (cudaStream_t)stream);
-    if (e != cudaSuccess) return cuda_bad(e, "balance workspace");
-  }
-  if (p.counted) {
-    const int n = std::min(cdiv(a.rows * a.top_k, BAL_THREADS * 2), 148);
-    const cudaError_t e = launch(balance_count_kernel, dim3(n), BAL_THREADS, 0, stream, p);
+  p.count_ctas = ctas > 1 ? std::min(cdiv(a.rows * a.top_k, 4 * BAL_COUNT_THREADS), BAL_COUNT_CTAS) : 0;
+  if (p.count_ctas) {
+    const cudaError_t e = launch(balance_count_kernel, dim3(p.count_ctas), BAL_COUNT_THREADS, 0, stream, p);
     if (e != cudaSuccess) return cuda_bad(e, "balance count launch");
   }
-  auto k = lanes == 2   ? balance_kernel<2, 1>
-           : lanes == 4  ? balance_kernel<4, 1>
-           : lanes == 8  ? balance_kernel<8, 1>
-           : lanes == 16 ? balance_kernel<16, 1>
-           : a.experts <= 128 ? balance_kernel<32, 1>
-                              : balance_kernel<32, 2>;
-  return done(launch(k, dim3(ctas), ctas == 1 ? BAL_ALONE : BAL_THREADS, 0, stream, p), "balance launch");
+  const bool sigmoid = a.score == TS_SCORE_SIGMOID_RENORM, wide = a.dtype == TS_DT_FP32;
+  auto k = sigmoid ? (wide ? balance_instance<true, true>(a.experts) : balance_instance<true, false>(a.experts))
+                   : (wide ? balance_instance<false, true>(a.experts) : balance_instance<false, false>(a.experts));
+  const int threads = (int64_t)a.rows * a.experts <= 4096 ? BAL_ALONE : BAL_THREADS;
+  return done(launch(k, dim3(ctas), threads, 0, stream, p), "balance launch");
 }
 
 }  // extern "C"
