@@ -264,16 +264,20 @@ def _check_op(st: int):
         raise TsMoeError(st, lib.ts_moe_last_error(None).decode())
 
 
-def _rows(t: torch.Tensor, what: str, rows: int, cols: int, dev: torch.device) -> int:
-    """The row stride of a [rows][cols] tensor on `dev` with a contiguous last dimension."""
-    if t.device != dev:
-        _refuse(f"{what} is on {t.device}, not on {dev}")
+def _rows(t: torch.Tensor, what: str, rows: int, cols: int, dev: int) -> int:
+    """The row stride of a [rows][cols] tensor on device `dev` (-1: the CPU) with a contiguous last dimension."""
+    if t.get_device() != dev:
+        _refuse(f"{what} is on {t.device}, not on {_name(dev)}")
     if t.shape != (rows, cols):
         _refuse(f"{what} has shape {tuple(t.shape)}, not {(rows, cols)}")
     ld, inner = t.stride()
     if inner != 1 and cols > 1:
         _refuse(f"{what} needs a contiguous last dimension")
-    return ld if rows > 1 and ld >= cols else max(ld, cols) if rows <= 1 else ld
+    return ld if rows > 1 else max(ld, cols)
+
+
+def _name(dev: int) -> str:
+    return "cpu" if dev < 0 else f"cuda:{dev}"
 
 
 def _type(t: torch.Tensor, what: str) -> int:
@@ -283,38 +287,43 @@ def _type(t: torch.Tensor, what: str) -> int:
     return dt
 
 
-def _flat(t: torch.Tensor, what: str, n: int, dtype, dev: torch.device) -> int:
-    if t.device != dev or t.dtype != dtype or t.numel() != n or not t.is_contiguous():
-        _refuse(f"{what} must be a contiguous {dtype} tensor of {n} elements on {dev}")
+def _flat(t: torch.Tensor, what: str, n: int, dtype, dev: int) -> int:
+    if t.get_device() != dev or t.dtype != dtype or t.numel() != n or not t.is_contiguous():
+        _refuse(f"{what} must be a contiguous {dtype} tensor of {n} elements on {_name(dev)}")
     return t.data_ptr()
 
 
+_CODES = (torch.float8_e4m3fn, torch.uint8)
+
+
 def _codes(t: torch.Tensor, what: str):
-    if t.dtype != torch.float8_e4m3fn and t.dtype != torch.uint8:
+    if t.dtype not in _CODES:
         _refuse(f"{what} is {t.dtype}; float8_e4m3fn (or its bytes as uint8) is needed")
 
 
-def _scales(t: torch.Tensor, what: str, shape: tuple, dev: torch.device) -> tuple:
-    if t.device != dev or t.dtype != torch.float32 or t.shape != shape:
-        _refuse(f"{what} must be a float32 tensor of shape {shape} on {dev}")
+def _scales(t: torch.Tensor, what: str, shape: tuple, dev: int) -> tuple:
+    if t.get_device() != dev or t.dtype != torch.float32 or t.shape != shape:
+        _refuse(f"{what} must be a float32 tensor of shape {shape} on {_name(dev)}")
     return t.stride()
 
 
-def _call(fn, args, dev: torch.device, stream):
+def _call(fn, args, dev: int, stream):
     """Calls on the tensors' own device and, without a stream, on that device's current stream."""
-    if dev.type != "cuda":
+    if dev < 0:
         _refuse("the tensors must be on a CUDA device")
     if stream is None:
-        stream = torch.cuda.current_stream(dev)
-    if isinstance(stream, torch.cuda.Stream):
-        if stream.device != dev:
-            _refuse(f"the stream belongs to {stream.device}, the tensors to {dev}")
+        stream = torch._C._cuda_getCurrentRawStream(dev)  # torch.cuda.current_stream(dev).cuda_stream takes 2 us
+    elif isinstance(stream, torch.cuda.Stream):
+        if stream.device.index != dev:
+            _refuse(f"the stream belongs to {stream.device}, the tensors to {_name(dev)}")
         stream = stream.cuda_stream
-    if torch.cuda.current_device() == dev.index:
-        _check_op(fn(C.byref(args), stream))
+    if torch.cuda.current_device() == dev:
+        st = fn(C.byref(args), stream)
     else:
         with torch.cuda.device(dev):
-            _check_op(fn(C.byref(args), stream))
+            st = fn(C.byref(args), stream)
+    if st != 0:
+        _check_op(st)
 
 
 def rmsnorm(resid: torch.Tensor, gamma: Optional[torch.Tensor], eps: float, delta: Optional[torch.Tensor] = None,
@@ -324,28 +333,29 @@ def rmsnorm(resid: torch.Tensor, gamma: Optional[torch.Tensor], eps: float, delt
     v = r / sqrt(mean(r^2) + eps) * gamma, written to y [M, H] and/or as 8-bit
     rows to q [M, H] with q_scale [M, ceil(H / 128)] (any strides)."""
     M, H = resid.shape
-    dev = resid.device
-    a = RmsnormArgs()
-    a.rows, a.hidden, a.eps = M, H, eps
-    a.resid, a.ld_resid, a.resid_type = resid.data_ptr(), _rows(resid, "resid", M, H, dev), _type(resid, "resid")
+    dev = resid.get_device()
+    rt = _type(resid, "resid")
+    ld = _rows(resid, "resid", M, H, dev)
+    pd = ldd = td = pg = tg = po = ldo = py = ldy = ty = pq = ldq = ps = qr = qg = 0
     if delta is not None:
-        a.delta, a.ld_delta, a.delta_type = delta.data_ptr(), _rows(delta, "delta", M, H, dev), _type(delta, "delta")
+        pd, ldd, td = delta.data_ptr(), _rows(delta, "delta", M, H, dev), _type(delta, "delta")
     if gamma is not None:
-        a.gamma, a.gamma_type = _flat(gamma, "gamma", H, gamma.dtype, dev), _type(gamma, "gamma")
+        pg, tg = _flat(gamma, "gamma", H, gamma.dtype, dev), _type(gamma, "gamma")
     if resid_out is not None:
         if resid_out.dtype != resid.dtype:
             _refuse("resid_out must have resid's type")
-        a.resid_out, a.ld_resid_out = resid_out.data_ptr(), _rows(resid_out, "resid_out", M, H, dev)
+        po, ldo = resid_out.data_ptr(), _rows(resid_out, "resid_out", M, H, dev)
     if y is not None:
-        a.y, a.ld_y, a.y_type = y.data_ptr(), _rows(y, "y", M, H, dev), _type(y, "y")
+        py, ldy, ty = y.data_ptr(), _rows(y, "y", M, H, dev), _type(y, "y")
     if q is not None:
         _codes(q, "q")
-        a.q, a.ld_q = q.data_ptr(), _rows(q, "q", M, H, dev)
+        pq, ldq = q.data_ptr(), _rows(q, "q", M, H, dev)
     if q_scale is not None:
-        a.qs_row, a.qs_group = _scales(q_scale, "q_scale", (M, -(-H // 128)), dev)
-        a.q_scale = q_scale.data_ptr()
+        qr, qg = _scales(q_scale, "q_scale", (M, -(-H // 128)), dev)
+        ps = q_scale.data_ptr()
     if M == 0:
         return
+    a = RmsnormArgs(M, H, rt, td, tg, ty, eps, resid.data_ptr(), ld, pd, ldd, pg, po, ldo, py, ldy, pq, ldq, ps, qr, qg)
     _call(lib.ts_moe_rmsnorm, a, dev, stream)
 
 
@@ -354,7 +364,7 @@ def act_quant(gate: torch.Tensor, up: torch.Tensor, act: int, q: torch.Tensor, q
     """ts_moe_act_quant: the activation of gate and up ([M, I], e.g. two halves
     of one product) as 8-bit rows q [M, I] with q_scale [M, ceil(I / 128)]."""
     M, inter = gate.shape
-    dev = gate.device
+    dev = gate.get_device()
     if up.dtype != gate.dtype:
         _refuse("gate and up must have one type")
     _codes(q, "q")
@@ -377,27 +387,28 @@ def fp8_matmul(a: torch.Tensor, a_scale: torch.Tensor, b: torch.Tensor, b_scale:
     use b[g], other rows of out are left as they were."""
     M, K = a.shape
     N = out.shape[1]
-    dev = a.device
+    dev = a.get_device()
     kb = -(-K // 128)
     _codes(a, "a")
     _codes(b, "b")
     sa = _scales(a_scale, "a_scale", (M, kb), dev)
     if offsets is None:
         G, group, ldb, off = 1, 0, _rows(b, "b", N, K, dev), None
-        sb = (0,) + tuple(_scales(b_scale, "b_scale", (-(-N // 128), kb), dev))
+        sb = (0, *_scales(b_scale, "b_scale", (-(-N // 128), kb), dev))
     else:
         if b.dim() != 3:
             _refuse("b must be [G, N, K] when offsets are given")
         G, group, ldb = b.shape[0], b.stride(0), _rows(b[0], "b[g]", N, K, dev)
         sb = _scales(b_scale, "b_scale", (G, -(-N // 128), kb), dev)
         off = _flat(offsets, "offsets", G + 1, torch.int32, dev)
-    p = Fp8MatmulArgs(M, N, K, G, _type(out, "out"), 0, a.data_ptr(), _rows(a, "a", M, K, dev), a_scale.data_ptr(), sa[0], sa[1],
-                      b.data_ptr(), ldb, group, b_scale.data_ptr(), sb[0], sb[1], sb[2], off)
-    p.out, p.ld_out = out.data_ptr(), _rows(out, "out", M, N, dev)
+    pa = lda = 0
     if add is not None:
         if add.dtype != out.dtype:
             _refuse("add must have out's type")
-        p.add, p.ld_add = add.data_ptr(), _rows(add, "add", M, N, dev)
+        pa, lda = add.data_ptr(), _rows(add, "add", M, N, dev)
+    p = Fp8MatmulArgs(M, N, K, G, _type(out, "out"), 0, a.data_ptr(), _rows(a, "a", M, K, dev), a_scale.data_ptr(), sa[0], sa[1],
+                      b.data_ptr(), ldb, group, b_scale.data_ptr(), sb[0], sb[1], sb[2], off, pa, lda,
+                      out.data_ptr(), _rows(out, "out", M, N, dev))
     if M == 0:
         return
     _call(lib.ts_moe_fp8_matmul, p, dev, stream)
@@ -413,39 +424,41 @@ def balance(logits: torch.Tensor, idx: torch.Tensor, score: int, loss: torch.Ten
     times dloss (float32, one element; None = 1).  mask: bool or uint8 [M], rows
     that count.  Without a workspace one is taken from torch's allocator."""
     M, E = logits.shape
-    dev = logits.device
+    dev = logits.get_device()
     K = idx.shape[-1]
     if idx.dtype != torch.int32:
         _refuse(f"idx is {idx.dtype}; int32 is needed")
-    a = BalanceArgs(M, E, K, score, _type(logits, "logits"), coef, logits.data_ptr(), _rows(logits, "logits", M, E, dev),
-                    idx.data_ptr(), _rows(idx, "idx", M, K, dev))
+    pm = pd = pp = po = pg = ldg = 0
     if mask is not None:
         if mask.dtype not in (torch.bool, torch.uint8):
             _refuse(f"mask is {mask.dtype}; bool or uint8 is needed")
-        a.mask = _flat(mask, "mask", M, mask.dtype, dev)
+        pm = _flat(mask, "mask", M, mask.dtype, dev)
     if dloss is not None:
-        a.dloss = _flat(dloss, "dloss", 1, torch.float32, dev)
-    a.loss = _flat(loss, "loss", 1, torch.float32, dev)
-    a.counts = _flat(counts, "counts", E, torch.int32, dev)
+        pd = _flat(dloss, "dloss", 1, torch.float32, dev)
     if prob is not None:
-        a.prob = _flat(prob, "prob", E, torch.float32, dev)
+        pp = _flat(prob, "prob", E, torch.float32, dev)
     if offsets is not None:
-        a.offsets = _flat(offsets, "offsets", E + 1, torch.int32, dev)
+        po = _flat(offsets, "offsets", E + 1, torch.int32, dev)
     if dlogits is not None:
         if dlogits.dtype != logits.dtype:
             _refuse("dlogits must have the type of logits")
-        a.dlogits, a.ld_dlogits = dlogits.data_ptr(), _rows(dlogits, "dlogits", M, E, dev)
-    need = lib.ts_moe_balance_workspace(M, E)
+        pg, ldg = dlogits.data_ptr(), _rows(dlogits, "dlogits", M, E, dev)
+    a = BalanceArgs(M, E, K, score, _type(logits, "logits"), coef, logits.data_ptr(), _rows(logits, "logits", M, E, dev),
+                    idx.data_ptr(), _rows(idx, "idx", M, K, dev), pm, pd, _flat(loss, "loss", 1, torch.float32, dev), pp,
+                    _flat(counts, "counts", E, torch.int32, dev), po, pg, ldg)
     if workspace is None:
-        s = stream if isinstance(stream, torch.cuda.Stream) else None
-        if stream is not None and s is None:
-            _refuse("a raw stream handle needs a workspace of the caller's")
-        if dev.type != "cuda":
+        if dev < 0:
             _refuse("the tensors must be on a CUDA device")
-        with torch.cuda.stream(s):   # None: the current stream
-            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-    elif workspace.device != dev or not workspace.is_contiguous():
-        _refuse(f"workspace must be a contiguous tensor on {dev}")
+        need = lib.ts_moe_balance_workspace(M, E)
+        if stream is None:
+            workspace = torch.empty(need, dtype=torch.uint8, device=logits.device)
+        elif isinstance(stream, torch.cuda.Stream):
+            with torch.cuda.stream(stream):
+                workspace = torch.empty(need, dtype=torch.uint8, device=logits.device)
+        else:
+            _refuse("a raw stream handle needs a workspace of the caller's")
+    elif workspace.get_device() != dev or not workspace.is_contiguous():
+        _refuse(f"workspace must be a contiguous tensor on {_name(dev)}")
     a.workspace, a.workspace_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
     _call(lib.ts_moe_balance, a, dev, stream)
 
