@@ -258,7 +258,7 @@ __global__ void __launch_bounds__(BAL_THREADS) balance_kernel(const BalanceParam
 #pragma unroll
         for (int i = 0; i < N; ++i) {
           const float u = ex2(min_nan(-LOG2E * l[i], 127.f));
-          slope[i] = l[i] < -88.f ? 1.f : u * rcp(1.f + u);
+          slope[i] = l[i] < -60.f ? 1.f : u * rcp(1.f + u);  // from e^87 on the reciprocal is below the normal range
           if (m < 0.f) t[i] = ex2(LOG2E * (l[i] - m)) * slope[i];
         }
         reduce();

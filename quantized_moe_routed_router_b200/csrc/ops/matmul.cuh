@@ -24,7 +24,7 @@ struct MatmulParams {
   ts_moe_fp8_matmul_args a;
   int kb;      // scale blocks of K
   int splits;  // fp8_stream_kernel: CTAs of a cluster, which share K
-  int out_map; // fp8_tile_kernel: out has a tensor map (rows at 16-byte boundaries)
+  int out_map; // fp8_tile_kernel: out has a tensor map (rows from 16-byte boundary to 16-byte boundary)
 };
 
 // ----------------------------------------------------------------------------- groups
@@ -150,10 +150,10 @@ TSM_DEV Tile locate_tile(const MatmulParams& p, const GroupTable& tab, int t) {
 }
 
 // A warp's 32 rows of a tile go out through `stage`: two boxes of 128 bytes of each row at a time, 16-byte place c of
-// row r at c ^ (r & 7) (the 128-byte swizzle, which also spreads rows over the banks).  Outputs at 16-byte places leave
-// by tensor-map stores, which run beside the next tile: all SMs reach their stores at about the same time, and stores
-// by the threads kept them from the next tile's sums until HBM had taken them.  Odd places and a group's last rows are
-// stored by the threads; `add` comes in the same way, a row's columns side by side.
+// row r at c ^ (r & 7) (the 128-byte swizzle, which also spreads rows over the banks).  Outputs from one 16-byte place to
+// another leave by tensor-map stores, which run beside the next tile: all SMs reach their stores at about the same
+// time, and stores by the threads kept them from the next tile's sums until HBM had taken them.  Odd places and a
+// group's last rows are stored by the threads; `add` comes in the same way, a row's columns side by side.
 TSM_DEV int stage_at(int r, int c) { return c / 8 * 256 + r * 8 + (c % 8 ^ (r & 7)); }
 
 // Rows of `bytes` bytes (at most 256) from the stage to dst, ld bytes apart, at any places that elements of 2 or 4 bytes

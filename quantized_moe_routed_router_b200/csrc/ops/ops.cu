@@ -121,7 +121,7 @@ bool encode_rows(CUtensorMap* m, const uint8_t* p, int k, int rows, int64_t ld, 
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Map of out for stores of 32 rows x 128 bytes; rows start at 16-byte boundaries.
+// Map of out for stores of 32 rows x 128 bytes; rows start and end at 16-byte boundaries.
 bool encode_out(CUtensorMap* m, const ts_moe_fp8_matmul_args& a) {
   const int es = dt_size(a.out_type);
   cuuint64_t dims[2] = {(cuuint64_t)a.n, (cuuint64_t)a.rows}, strides[1] = {(cuuint64_t)a.ld_out * es};
@@ -306,7 +306,9 @@ ts_moe_status ts_moe_fp8_matmul(const ts_moe_fp8_matmul_args* args, void* stream
   }
   const bool tile = plan.kind == MatmulPlan::TILE;
   CUtensorMap ma, mb, mo = {};
-  p.out_map = tile && aligned(a.out, a.ld_out * dt_size(a.out_type), 16) && a.ld_out < (int64_t)1 << 37;
+  // a map's stores end at 16-byte places, not at elements: rows of another length would write past their end
+  const int es = dt_size(a.out_type);
+  p.out_map = tile && aligned(a.out, a.ld_out * es, 16) && (int64_t)a.n * es % 16 == 0 && a.ld_out < (int64_t)1 << 37;
   if (!encode_rows(&ma, a.a, a.k, a.rows, ld_a, -1, 0, tile ? TL_M : plan.bt) ||
       !encode_rows(&mb, a.b, a.k, a.n, ld_b, a.num_groups, group, tile ? TL_N : ST_N) || (p.out_map && !encode_out(&mo, a)))
     return set_last_error(TS_MOE_ECUDA, "fp8_matmul: the driver refused a tensor map");

@@ -567,3 +567,143 @@ def test_row_offsets_past_32_bits(B):
     R.check_rows8(q[-3:], s[-3:], v, NORM_REL)
     B.act_quant(buf[:, :8192], buf[:, 8192:], 0, q[:, :8192], s[:, :64])
     R.check_rows8(q[-3:, :8192], s[-3:, :64], R.act(tail[:, :8192], tail[:, 8192:], 0), ACT_REL)
+
+
+# ----------------------------------------------------------------------------- kernels and paths by size
+
+def nan_padded(q, pad, shift):
+    """8-bit rows in a buffer that holds NaN codes around them."""
+    M, K = q.shape
+    ld = -(-(K + pad + shift) // 16) * 16
+    buf = torch.full((M, ld), 0x7F, dtype=torch.uint8, device="cuda").view(torch.float8_e4m3fn)
+    at = buf[:, shift:shift + K]
+    at.copy_(q)
+    return at
+
+
+@pytest.mark.parametrize("M", [1, 2, 5, 7, 8, 9])
+@pytest.mark.parametrize("N,K", [(1, 1), (15, 17), (16, 16), (17, 127), (31, 144), (2049, 129), (640, 4096), (1000, 1100), (48, 14336)])
+def test_fp8_matmul_a_step_of_decode(B, M, N, K):
+    """Few rows, with NaN codes behind every row of both operands."""
+    r = gen(M + N + K)
+    qa, sa = R.encode_rows(r(M, K))
+    qb, sb = R.encode_matrix(0.05 * r(N, K))
+    check_matmul(B, M, N, K, (BF16, FP16, FP32)[(M + K) % 3], add=(None, True, "in place")[(M + N) % 3],
+                 a=(nan_padded(qa, 5, 16), sa), b=(nan_padded(qb, 33, 0), sb))
+
+
+@pytest.mark.parametrize("out_type", [BF16, FP16, FP32])
+@pytest.mark.parametrize("add", [None, True, "in place"])
+@pytest.mark.parametrize("N", [2049, 2050, 2056])
+def test_fp8_matmul_tiles_at_odd_places(B, N, add, out_type):
+    """Tiles whose rows start at 2-, 4- and 16-byte places, plain and added to."""
+    check_matmul(B, 2500, N, 1408, out_type, add=add)
+
+
+@pytest.mark.parametrize("out_type", [BF16, FP32])
+@pytest.mark.parametrize("shift", [0, 1, 3, 6])
+def test_fp8_matmul_tiles_leave_their_surroundings(B, out_type, shift):
+    """Groups whose last rows end inside a tile, written into a wider buffer: nothing beside them changes."""
+    sizes, N, K = [200, 0, 333, 1, 150], 300, 256
+    M = sum(sizes) + 7
+    r = gen(shift)
+    a, sa = R.encode_rows(r(M, K))
+    b = torch.zeros(len(sizes), N, K, dtype=torch.uint8, device="cuda").view(torch.float8_e4m3fn)
+    sb = torch.empty(len(sizes), R.blocks(N), R.blocks(K), device="cuda")
+    for g in range(len(sizes)):
+        q, s = R.encode_matrix(0.05 * r(N, K))
+        b[g].copy_(q)
+        sb[g].copy_(s)
+    edge = [0]
+    for s in sizes:
+        edge.append(edge[-1] + s)
+    buf = torch.full((M + 2, N + 12), 7.0, dtype=out_type, device="cuda")
+    out = buf[1:-1, shift:shift + N]
+    B.fp8_matmul(a, sa, b, sb, out, offsets=torch.tensor(edge, dtype=torch.int32, device="cuda"))
+    da = R.dequant_rows(a, sa)
+    for g in range(len(sizes)):
+        lo, hi = edge[g], edge[g + 1]
+        v, mags = R.matmul(da[lo:hi], R.dequant_matrix(b[g], sb[g]))
+        assert ((R.d64(out[lo:hi]) - v).abs() <= R.matmul_tol(v, mags, K, out_type)).all(), g
+    assert (out[edge[-1]:] == 7).all() and (buf[0] == 7).all() and (buf[-1] == 7).all()
+    assert (buf[:, :shift] == 7).all() and (buf[:, shift + N:] == 7).all()
+
+
+@pytest.mark.parametrize("M,H,rt,dt", [(2000, 512, BF16, FP32), (1300, 4096, BF16, BF16), (1100, 8192, FP32, FP32), (1200, 5120, FP16, BF16)])
+def test_rmsnorm_many_rows_in_place(B, M, H, rt, dt):
+    """More rows than CTAs, the residual in place and rows inside a wider buffer."""
+    r = gen(M + H)
+    buf = torch.full((M, H + 16), 9.0, dtype=rt, device="cuda")
+    at = buf[:, 8:8 + H]
+    at.copy_((r(M, H) * torch.exp(r(M, 1))).to(rt))
+    delta, gamma = r(M, H).to(dt), (1 + 0.2 * r(H)).to(BF16)
+    want_r, v = R.rmsnorm(at, gamma, 1e-5, delta)
+    y, q, s = torch.empty(M, H, dtype=BF16, device="cuda"), R.rows8(M, H), torch.empty(M, R.blocks(H), device="cuda")
+    B.rmsnorm(at, gamma, 1e-5, delta=delta, resid_out=at, y=y, q=q, q_scale=s)
+    assert torch.equal(at.cpu(), want_r)
+    assert ((R.d64(y) - v).abs() <= R.rounding(v, BF16) + v.abs() * NORM_REL).all()
+    R.check_rows8(q, s, v, NORM_REL)
+    assert (buf[:, :8] == 9).all() and (buf[:, 8 + H:] == 9).all()
+
+
+@pytest.mark.parametrize("dtype", [FP32, BF16])
+@pytest.mark.parametrize("E", [8, 60, 129, 256])
+def test_balance_rows_of_unlike_size(B, E, dtype):
+    """Rows whose sigmoids all but vanish beside ordinary ones, in one warp and far from E = a multiple of four."""
+    l, idx = routed(700, E, 4)
+    l[::3] -= 30
+    l[1::5] -= 95
+    l[7] = -1e4
+    l[8, 1:] = -float("inf")
+    l = l.to(dtype)
+    mask = torch.rand(700, generator=torch.Generator().manual_seed(E)).cuda() > 0.2
+    for score in (1, 2):
+        check_balance(B, l, idx, score, mask=mask, coef=0.3)
+        check_balance(B, l[:20], idx[:20], score)
+
+
+def test_balance_masked_rows_may_hold_anything(B):
+    """Rows that the mask leaves out may hold NaN and infinities: they touch nothing."""
+    l, idx = routed(600, 64, 6)
+    mask = torch.ones(600, dtype=torch.bool, device="cuda")
+    mask[100:140] = False
+    for score in (1, 2):
+        want = run_balance(B, torch.where(mask[:, None], l, torch.zeros_like(l)), idx, score, mask)
+        bad = l.clone()
+        bad[100:120], bad[120:130], bad[130:140] = float("nan"), float("inf"), -float("inf")
+        got = run_balance(B, bad, idx, score, mask)
+        for x, y in zip(got, want):
+            assert torch.equal(x, y)
+        assert not got[-1][100:140].any()
+
+
+def test_two_graphs_replayed_in_turn(B):
+    """Two captured calls of one size, each with its own inputs: replays in turn equal eager calls."""
+    cases = []
+    for seed in (1, 2):
+        l, idx = routed(9000, 64, 6, seed=seed)
+        a, sa = R.encode_rows(gen(seed)(300, 512))
+        b, sb = R.encode_matrix(gen(seed + 9)(700, 512))
+        out, loss = torch.empty(300, 700, device="cuda"), torch.empty(1, device="cuda")
+        counts, d = torch.empty(64, dtype=torch.int32, device="cuda"), torch.empty_like(l)
+
+        def call(l=l, idx=idx, a=a, sa=sa, b=b, sb=sb, out=out, loss=loss, counts=counts, d=d):
+            B.balance(l, idx, 2, loss, counts, dlogits=d)
+            B.fp8_matmul(a, sa, b, sb, out)
+            return out, loss, counts, d
+
+        want = [t.clone() for t in call()]
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            got = call()
+        cases.append((graph, got, want, call))   # call keeps the inputs alive
+    for _ in range(3):
+        for graph, got, *_ in cases:
+            for t in got:
+                t.zero_()
+            graph.replay()
+        torch.cuda.synchronize()
+        for _, got, want, _ in cases:
+            for x, y in zip(got, want):
+                assert torch.equal(x, y)
