@@ -21,7 +21,7 @@ struct Raw8 {
 };
 
 // Loads elements [off, off + n) of a row, n <= 8.  VEC: n = 8 and the address
-// is 16-byte aligned; otherwise element by element, the rest zero.
+// is 16-byte aligned; otherwise at whatever place an element can have, the rest zero.
 template <bool VEC>
 TSM_DEV Raw8 load_raw8(const void* base, int type, int64_t off, int n) {
   Raw8 r;
@@ -40,6 +40,17 @@ TSM_DEV Raw8 load_raw8(const void* base, int type, int64_t off, int n) {
 #pragma unroll
     for (int j = 0; j < 8; ++j)
       if (j < n) w[j] = ((const uint32_t*)base)[off + j];
+  } else if (n == 8) {
+    // four words, or three between two halves where the row starts at an odd element
+    const uint16_t* p = (const uint16_t*)base + off;
+    if ((uintptr_t)p % 4 == 0) {
+      const uint32_t* q = (const uint32_t*)p;
+      w[0] = q[0], w[1] = q[1], w[2] = q[2], w[3] = q[3];
+    } else {
+      const uint32_t* q = (const uint32_t*)(p + 1);
+      const uint32_t a = q[0], b = q[1], c = q[2], first = p[0], last = p[7];
+      w[0] = first | a << 16, w[1] = a >> 16 | b << 16, w[2] = b >> 16 | c << 16, w[3] = c >> 16 | last << 16;
+    }
   } else {
 #pragma unroll
     for (int j = 0; j < 8; ++j)
@@ -150,6 +161,16 @@ TSM_DEV void store_raw8(void* base, int type, int64_t off, int n, const Raw8& r)
 #pragma unroll
     for (int j = 0; j < 8; ++j)
       if (j < n) ((uint32_t*)base)[off + j] = w[j];
+  } else if (n == 8) {
+    uint16_t* p = (uint16_t*)base + off;
+    if ((uintptr_t)p % 4 == 0) {
+      uint32_t* q = (uint32_t*)p;
+      q[0] = w[0], q[1] = w[1], q[2] = w[2], q[3] = w[3];
+    } else {
+      uint32_t* q = (uint32_t*)(p + 1);
+      p[0] = (uint16_t)w[0], p[7] = (uint16_t)(w[3] >> 16);
+      q[0] = w[0] >> 16 | w[1] << 16, q[1] = w[1] >> 16 | w[2] << 16, q[2] = w[2] >> 16 | w[3] << 16;
+    }
   } else {
 #pragma unroll
     for (int j = 0; j < 8; ++j)
@@ -219,6 +240,8 @@ TSM_DEV void quant_group(const float (&v)[16 / LANES][8], uint8_t* q, int64_t of
     const int nc = n - c * LANES * 8;
     if (VEC) {
       if (nc > 0) *(uint2*)(q + at) = make_uint2(w[0], w[1]);
+    } else if (nc >= 8 && (uintptr_t)(q + at) % 8 == 0) {
+      *(uint2*)(q + at) = make_uint2(w[0], w[1]);
     } else {
 #pragma unroll
       for (int j = 0; j < 8; ++j)
