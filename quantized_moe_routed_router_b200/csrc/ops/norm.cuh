@@ -12,9 +12,7 @@
 
 namespace tsm {
 
-// Threads of the largest row's CTA: one or two chunks per thread for few rows, four for many.
-template <int IT>
-constexpr int NORM_MAX_THREADS = IT == 4 ? 512 : 1024;
+constexpr int NORM_MAX_THREADS = 1024;
 
 // Sum over the CTA; `slots` holds one value a warp and must not be written again before the next barrier but one.
 TSM_DEV float norm_cta_sum(float x, float* slots) {
@@ -32,8 +30,8 @@ TSM_DEV float norm_cta_sum(float x, float* slots) {
 // One CTA per row; thread t holds the eight-column chunks t, t + blockDim.x, ...
 // (IT of them), so sixteen neighbouring lanes hold one 128-column scale group.
 template <int IT, bool VEC>
-__global__ void __launch_bounds__(NORM_MAX_THREADS<IT>) rmsnorm_kernel(const ts_moe_rmsnorm_args a) {
-  __shared__ float warp_sum[NORM_MAX_THREADS<IT> / 32];
+__global__ void __launch_bounds__(NORM_MAX_THREADS) rmsnorm_kernel(const ts_moe_rmsnorm_args a) {
+  __shared__ float warp_sum[NORM_MAX_THREADS / 32];
   grid_dep_wait();
   grid_dep_launch();
   const int64_t row = blockIdx.x;

@@ -196,11 +196,9 @@ cudaError_t launch_norm(const ts_moe_rmsnorm_args& a, bool vec, void* stream) {
     return a.hidden <= 4096   ? launch_norm_rows<256>(a, stream)
            : a.hidden <= 8192 ? launch_norm_rows<512>(a, stream)
                               : launch_norm_rows<1024>(a, stream);
-  const int it = a.rows <= 1024 ? (chunks <= 1024 ? 1 : 2) : 4;
+  const int it = chunks <= 1024 ? 1 : 2;
   const int threads = std::max(32, cdiv(cdiv(chunks, it), 32) * 32);
-  auto k = it == 1   ? (vec ? rmsnorm_kernel<1, true> : rmsnorm_kernel<1, false>)
-           : it == 2 ? (vec ? rmsnorm_kernel<2, true> : rmsnorm_kernel<2, false>)
-                     : rmsnorm_kernel<4, false>;
+  auto k = it == 1 ? (vec ? rmsnorm_kernel<1, true> : rmsnorm_kernel<1, false>) : (vec ? rmsnorm_kernel<2, true> : rmsnorm_kernel<2, false>);
   return launch(k, dim3(a.rows), threads, 0, stream, a);
 }
 
