@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import ctypes as C
 import os
+import struct
 from typing import Optional, Sequence
 
 import numpy as np
@@ -307,23 +308,43 @@ def _scales(t: torch.Tensor, what: str, shape: tuple, dev: int) -> tuple:
     return t.stride()
 
 
-def _call(fn, args, dev: int, stream):
-    """Calls on the tensors' own device and, without a stream, on that device's current stream."""
-    if dev < 0:
-        _refuse("the tensors must be on a CUDA device")
-    if stream is None:
-        stream = torch._C._cuda_getCurrentRawStream(dev)  # torch.cuda.current_stream(dev).cuda_stream takes 2 us
-    elif isinstance(stream, torch.cuda.Stream):
-        if stream.device.index != dev:
-            _refuse(f"the stream belongs to {stream.device}, the tensors to {_name(dev)}")
-        stream = stream.cuda_stream
-    if torch.cuda.current_device() == dev:
-        st = fn(C.byref(args), stream)
-    else:
-        with torch.cuda.device(dev):
-            st = fn(C.byref(args), stream)
-    if st != 0:
-        _check_op(st)
+class _Op:
+    """An entry point whose argument struct is packed in one go: building the ctypes struct costs a decode step's call
+    about a microsecond more."""
+
+    def __init__(self, name: str, fmt: str, args: type):
+        self.pack = struct.Struct(fmt).pack
+        assert struct.calcsize(fmt) == C.sizeof(args)
+        self.fn = lib[name]      # a function object of its own: the struct goes in as bytes
+        self.fn.argtypes, self.fn.restype = [C.c_char_p, C.c_void_p], C.c_int
+
+    def __call__(self, dev: int, stream, *fields):
+        """Calls on the tensors' own device and, without a stream, on that device's current stream."""
+        if dev < 0:
+            _refuse("the tensors must be on a CUDA device")
+        if stream is None:
+            stream = torch._C._cuda_getCurrentRawStream(dev)  # torch.cuda.current_stream(dev).cuda_stream takes 2 us
+        elif isinstance(stream, torch.cuda.Stream):
+            if stream.device.index != dev:
+                _refuse(f"the stream belongs to {stream.device}, the tensors to {_name(dev)}")
+            stream = stream.cuda_stream
+        try:
+            args = self.pack(*fields)
+        except struct.error as e:
+            _refuse(f"an argument does not fit its field: {e}")
+        if torch.cuda.current_device() == dev:
+            st = self.fn(args, stream)
+        else:
+            with torch.cuda.device(dev):
+                st = self.fn(args, stream)
+        if st != 0:
+            _check_op(st)
+
+
+_rmsnorm = _Op("ts_moe_rmsnorm", "@6ifPqPqPPqPqPqPqq", RmsnormArgs)
+_act_quant = _Op("ts_moe_act_quant", "@4i2fPqPqPqPqq", ActQuantArgs)
+_fp8_matmul = _Op("ts_moe_fp8_matmul", "@6iPqPqqPqqPqqqPPqPq", Fp8MatmulArgs)
+_balance = _Op("ts_moe_balance", "@5ifPqPqPPPPPPPqPQ", BalanceArgs)
 
 
 def rmsnorm(resid: torch.Tensor, gamma: Optional[torch.Tensor], eps: float, delta: Optional[torch.Tensor] = None,
@@ -355,8 +376,7 @@ def rmsnorm(resid: torch.Tensor, gamma: Optional[torch.Tensor], eps: float, delt
         ps = q_scale.data_ptr()
     if M == 0:
         return
-    a = RmsnormArgs(M, H, rt, td, tg, ty, eps, resid.data_ptr(), ld, pd, ldd, pg, po, ldo, py, ldy, pq, ldq, ps, qr, qg)
-    _call(lib.ts_moe_rmsnorm, a, dev, stream)
+    _rmsnorm(dev, stream, M, H, rt, td, tg, ty, eps, resid.data_ptr(), ld, pd, ldd, pg, po, ldo, py, ldy, pq, ldq, ps, qr, qg)
 
 
 def act_quant(gate: torch.Tensor, up: torch.Tensor, act: int, q: torch.Tensor, q_scale: torch.Tensor,
@@ -369,12 +389,12 @@ def act_quant(gate: torch.Tensor, up: torch.Tensor, act: int, q: torch.Tensor, q
         _refuse("gate and up must have one type")
     _codes(q, "q")
     qs = _scales(q_scale, "q_scale", (M, -(-inter // 128)), dev)
-    a = ActQuantArgs(M, inter, act, _type(gate, "gate"), act_alpha, act_limit,
-                     gate.data_ptr(), _rows(gate, "gate", M, inter, dev), up.data_ptr(), _rows(up, "up", M, inter, dev),
-                     q.data_ptr(), _rows(q, "q", M, inter, dev), q_scale.data_ptr(), qs[0], qs[1])
+    fields = (M, inter, act, _type(gate, "gate"), act_alpha, act_limit,
+              gate.data_ptr(), _rows(gate, "gate", M, inter, dev), up.data_ptr(), _rows(up, "up", M, inter, dev),
+              q.data_ptr(), _rows(q, "q", M, inter, dev), q_scale.data_ptr(), qs[0], qs[1])
     if M == 0:
         return
-    _call(lib.ts_moe_act_quant, a, dev, stream)
+    _act_quant(dev, stream, *fields)
 
 
 def fp8_matmul(a: torch.Tensor, a_scale: torch.Tensor, b: torch.Tensor, b_scale: torch.Tensor, out: torch.Tensor,
@@ -393,7 +413,7 @@ def fp8_matmul(a: torch.Tensor, a_scale: torch.Tensor, b: torch.Tensor, b_scale:
     _codes(b, "b")
     sa = _scales(a_scale, "a_scale", (M, kb), dev)
     if offsets is None:
-        G, group, ldb, off = 1, 0, _rows(b, "b", N, K, dev), None
+        G, group, ldb, off = 1, 0, _rows(b, "b", N, K, dev), 0
         sb = (0, *_scales(b_scale, "b_scale", (-(-N // 128), kb), dev))
     else:
         if b.dim() != 3:
@@ -406,12 +426,11 @@ def fp8_matmul(a: torch.Tensor, a_scale: torch.Tensor, b: torch.Tensor, b_scale:
         if add.dtype != out.dtype:
             _refuse("add must have out's type")
         pa, lda = add.data_ptr(), _rows(add, "add", M, N, dev)
-    p = Fp8MatmulArgs(M, N, K, G, _type(out, "out"), 0, a.data_ptr(), _rows(a, "a", M, K, dev), a_scale.data_ptr(), sa[0], sa[1],
-                      b.data_ptr(), ldb, group, b_scale.data_ptr(), sb[0], sb[1], sb[2], off, pa, lda,
-                      out.data_ptr(), _rows(out, "out", M, N, dev))
+    fields = (M, N, K, G, _type(out, "out"), 0, a.data_ptr(), _rows(a, "a", M, K, dev), a_scale.data_ptr(), *sa,
+              b.data_ptr(), ldb, group, b_scale.data_ptr(), *sb, off, pa, lda, out.data_ptr(), _rows(out, "out", M, N, dev))
     if M == 0:
         return
-    _call(lib.ts_moe_fp8_matmul, p, dev, stream)
+    _fp8_matmul(dev, stream, *fields)
 
 
 def balance(logits: torch.Tensor, idx: torch.Tensor, score: int, loss: torch.Tensor, counts: torch.Tensor,
@@ -443,9 +462,9 @@ def balance(logits: torch.Tensor, idx: torch.Tensor, score: int, loss: torch.Ten
         if dlogits.dtype != logits.dtype:
             _refuse("dlogits must have the type of logits")
         pg, ldg = dlogits.data_ptr(), _rows(dlogits, "dlogits", M, E, dev)
-    a = BalanceArgs(M, E, K, score, _type(logits, "logits"), coef, logits.data_ptr(), _rows(logits, "logits", M, E, dev),
-                    idx.data_ptr(), _rows(idx, "idx", M, K, dev), pm, pd, _flat(loss, "loss", 1, torch.float32, dev), pp,
-                    _flat(counts, "counts", E, torch.int32, dev), po, pg, ldg)
+    fields = (M, E, K, score, _type(logits, "logits"), coef, logits.data_ptr(), _rows(logits, "logits", M, E, dev),
+              idx.data_ptr(), _rows(idx, "idx", M, K, dev), pm, pd, _flat(loss, "loss", 1, torch.float32, dev), pp,
+              _flat(counts, "counts", E, torch.int32, dev), po, pg, ldg)
     if workspace is None:
         if dev < 0:
             _refuse("the tensors must be on a CUDA device")
@@ -459,8 +478,7 @@ def balance(logits: torch.Tensor, idx: torch.Tensor, score: int, loss: torch.Ten
             _refuse("a raw stream handle needs a workspace of the caller's")
     elif workspace.get_device() != dev or not workspace.is_contiguous():
         _refuse(f"workspace must be a contiguous tensor on {_name(dev)}")
-    a.workspace, a.workspace_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
-    _call(lib.ts_moe_balance, a, dev, stream)
+    _balance(dev, stream, *fields, workspace.data_ptr(), workspace.numel() * workspace.element_size())
 
 
 def validate(shape: "synth.MoEShape", layers: Sequence["synth.LayerBlobs"], **cfg_over) -> tuple:
