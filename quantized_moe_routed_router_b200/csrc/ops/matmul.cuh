@@ -11,7 +11,7 @@
 //   fp8_tile_kernel    128 rows x 256 columns per CTA, persistent.
 //   fp8_stream_kernel  128 columns x 16 or 32 rows per CTA with the matrix as the MMA's first operand, K split
 //                      over a cluster: few rows, where reading the matrix bounds it.
-//   fp8_row_kernel     16 columns x up to 8 rows per CTA, K split over its warps, the matrix from global memory
+//   fp8_row_kernel     16 columns x up to 16 rows per CTA, K split over its warps, the matrix from global memory
 //                      straight into registers: the shortest way for a decode step's rows.
 #pragma once
 #include "umma.cuh"
@@ -708,8 +708,7 @@ __global__ void __launch_bounds__(ST_THREADS, StreamShape<BT>::CTAS)
 // MMA's, tokens its columns.  Which k stands at which place of a fragment is free as long as both operands agree, so a
 // lane takes sixteen neighbouring codes of a row and they serve four MMAs.  Registers, one barrier and no other
 // set-up: at 16 x 1024 x 2048 fp8_stream_kernel takes 8.2 us of which 0.3 us are traffic.
-constexpr int RW_N = 16, RW_WARPS = 8, RW_THREADS = 32 * RW_WARPS, RW_MAX_ROWS = 8;
-constexpr int RW_AHEAD = 3;  // scale blocks of the matrix on their way to a warp
+constexpr int RW_N = 16, RW_MAX_ROWS = 16, RW_WARPS = 8, RW_THREADS = 32 * RW_WARPS;
 
 // Sixteen codes from `at` of a row of k; past k they are zeros.
 TSM_DEV uint4 load_codes(const uint8_t* row, int at, int k, bool in) {
@@ -732,8 +731,11 @@ TSM_DEV uint2 e4m3x4_to_f16(uint32_t w) {
   return r;
 }
 
+// NT: groups of eight tokens.  The CTA's warps share K.
+template <int NT>
 __global__ void __launch_bounds__(RW_THREADS, 2) fp8_row_kernel(const MatmulParams p) {
-  __shared__ float red[RW_WARPS][RW_MAX_ROWS][RW_N + 1];
+  constexpr int AHEAD = NT == 1 ? 3 : 2;  // scale blocks of the matrix on their way to a warp
+  __shared__ float red[RW_WARPS][8 * NT][RW_N + 1];
   const ts_moe_fp8_matmul_args& a = p.a;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
   const int n0 = blockIdx.x * RW_N;
@@ -743,9 +745,9 @@ __global__ void __launch_bounds__(RW_THREADS, 2) fp8_row_kernel(const MatmulPara
   const uint8_t* w0 = a.b + (int64_t)(n0 + g) * a.ld_b;
   const uint8_t* w1 = w0 + 8 * a.ld_b;
   const bool in0 = n0 + g < a.n, in1 = n0 + g + 8 < a.n;
-  // lane (g, c) holds codes 64 h + 16 c .. + 15 of a block, h = 0, 1, of its two rows and of token g
-  uint4 A[RW_AHEAD][2][2], X[2][2];
-  float sa[2][2], sb[2];
+  // lane (g, c) holds codes 64 h + 16 c .. + 15 of a block, h = 0, 1, of its two rows and of tokens g, g + 8
+  uint4 A[AHEAD][2][2], X[2][NT][2];
+  float sa[2][NT][2], sb[2];
   auto fetch_a = [&](int b, uint4 (&f)[2][2]) {
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
@@ -756,26 +758,34 @@ __global__ void __launch_bounds__(RW_THREADS, 2) fp8_row_kernel(const MatmulPara
   };
   auto fetch_x = [&](int b, int buf) {
 #pragma unroll
-    for (int h = 0; h < 2; ++h)
-      X[buf][h] = load_codes(a.a + (int64_t)g * a.ld_a, b < b1 ? b * SCALE_BLOCK + h * 64 + c * 16 : a.k, a.k, g < a.rows);
+    for (int t = 0; t < NT; ++t) {
+      const int m = t * 8 + g;
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      const int q = c * 2 + j;  // the tokens of this lane's sums
-      sa[buf][j] = b < b1 && q < a.rows ? a.a_scale[(int64_t)q * a.as_row + (int64_t)b * a.as_block] : 0.f;
+      for (int h = 0; h < 2; ++h)
+        X[buf][t][h] = load_codes(a.a + (int64_t)m * a.ld_a, b < b1 ? b * SCALE_BLOCK + h * 64 + c * 16 : a.k, a.k, m < a.rows);
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const int q = t * 8 + c * 2 + j;  // the tokens of this lane's sums
+        sa[buf][t][j] = b < b1 && q < a.rows ? a.a_scale[(int64_t)q * a.as_row + (int64_t)b * a.as_block] : 0.f;
+      }
     }
     sb[buf] = b < b1 ? a.b_scale[(int64_t)(n0 / SCALE_BLOCK) * a.bs_row + (int64_t)b * a.bs_block] : 0.f;
   };
-  float acc[4] = {0.f, 0.f, 0.f, 0.f};
+  float acc[NT][4];
 #pragma unroll
-  for (int i = 0; i < RW_AHEAD; ++i) fetch_a(b0 + i, A[i]);
+  for (int t = 0; t < NT; ++t) acc[t][0] = acc[t][1] = acc[t][2] = acc[t][3] = 0.f;
+#pragma unroll
+  for (int i = 0; i < AHEAD; ++i) fetch_a(b0 + i, A[i]);
   fetch_x(b0, 0);
-  for (int b = b0; b < b1; b += 2 * RW_AHEAD) {
+  for (int b = b0; b < b1; b += 2 * AHEAD) {
 #pragma unroll
-    for (int i = 0; i < 2 * RW_AHEAD; ++i) {  // an even number of steps: buffers of X and slots of A by constants
+    for (int i = 0; i < 2 * AHEAD; ++i) {  // an even number of steps: buffers of X and slots of A by constants
       if (b + i >= b1) break;
-      const int buf = i & 1, slot = i % RW_AHEAD;
+      const int buf = i & 1, slot = i % AHEAD;
       fetch_x(b + i + 1, buf ^ 1);
-      float P[4] = {0.f, 0.f, 0.f, 0.f};
+      float P[NT][4];
+#pragma unroll
+      for (int t = 0; t < NT; ++t) P[t][0] = P[t][1] = P[t][2] = P[t][3] = 0.f;
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         const uint32_t r0[4] = {A[slot][h][0].x, A[slot][h][0].y, A[slot][h][0].z, A[slot][h][0].w};
@@ -784,26 +794,38 @@ __global__ void __launch_bounds__(RW_THREADS, 2) fp8_row_kernel(const MatmulPara
         for (int s = 0; s < 4; ++s) {
           const uint2 lo = e4m3x4_to_f16(r0[s]), hi = e4m3x4_to_f16(r1[s]);
           const uint32_t fa[4] = {lo.x, hi.x, lo.y, hi.y};
-          const uint4 x = X[buf][h];
-          const uint2 fx = e4m3x4_to_f16(s == 0 ? x.x : s == 1 ? x.y : s == 2 ? x.z : x.w);
-          mma_f16_acc(P, fa, fx.x, fx.y);
+#pragma unroll
+          for (int t = 0; t < NT; ++t) {
+            const uint4 x = X[buf][t][h];
+            const uint2 fx = e4m3x4_to_f16(s == 0 ? x.x : s == 1 ? x.y : s == 2 ? x.z : x.w);
+            mma_f16_acc(P[t], fa, fx.x, fx.y);
+          }
         }
       }
-      fetch_a(b + i + RW_AHEAD, A[slot]);
+      fetch_a(b + i + AHEAD, A[slot]);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) acc[j] += sa[buf][j & 1] * sb[buf] * P[j];
+      for (int t = 0; t < NT; ++t) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) acc[t][j] += sa[buf][t][j & 1] * sb[buf] * P[t][j];
+      }
     }
   }
   // D: rows g and g + 8 of the matrix, tokens 2c and 2c + 1
 #pragma unroll
-  for (int j = 0; j < 4; ++j) red[warp][c * 2 + (j & 1)][g + 8 * (j >> 1)] = acc[j];
-  __syncthreads();
-  const int m = threadIdx.x / RW_N, n = threadIdx.x % RW_N;
-  if (m < a.rows && n0 + n < a.n) {
-    float v = a.add ? load1(a.add, a.out_type, (int64_t)m * a.ld_add + n0 + n) : 0.f, s = 0.f;
+  for (int t = 0; t < NT; ++t) {
 #pragma unroll
-    for (int q = 0; q < RW_WARPS; ++q) s += red[q][m][n];
-    store1(a.out, a.out_type, (int64_t)m * a.ld_out + n0 + n, s + v);
+    for (int j = 0; j < 4; ++j) red[warp][t * 8 + c * 2 + (j & 1)][g + 8 * (j >> 1)] = acc[t][j];
+  }
+  __syncthreads();
+#pragma unroll
+  for (int i = threadIdx.x; i < 8 * NT * RW_N; i += RW_THREADS) {
+    const int m = i / RW_N, n = i % RW_N;
+    if (m < a.rows && n0 + n < a.n) {
+      float v = a.add ? load1(a.add, a.out_type, (int64_t)m * a.ld_add + n0 + n) : 0.f, s = 0.f;
+#pragma unroll
+      for (int q = 0; q < RW_WARPS; ++q) s += red[q][m][n];
+      store1(a.out, a.out_type, (int64_t)m * a.ld_out + n0 + n, s + v);
+    }
   }
 }
 

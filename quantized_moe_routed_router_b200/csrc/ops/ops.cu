@@ -153,8 +153,13 @@ MatmulPlan matmul_plan(const ts_moe_fp8_matmul_args& a, int sms) {
   const int64_t mean = cdiv(a.rows, (int)reached);
   const int64_t tiles = (cdiv(a.rows, TL_M) + reached - 1) * cdiv(a.n, TL_N);
   const MatmulPlan tile = {MatmulPlan::TILE, 0, 1, (int)std::min<int64_t>(tiles, sms)};
-  // 1 x 4096 x 4096 6.2 against 8.9 by fp8_stream_kernel; with a second group of eight rows 10.4 against 9.0 (16 x 5760 x 2880)
-  if (!a.offsets && a.rows <= RW_MAX_ROWS) return {MatmulPlan::ROWS, 0, 1, cdiv(a.n, RW_N)};
+  // A decode step: without set-up, while the matrix is small enough for that to count and the CTAs run at once (against
+  // fp8_stream_kernel: 1 x 4096 x 4096 6.2 : 8.8, 8 x 5760 x 2880 8.1 : 8.9, 16 x 4096 x 4096 8.2 : 9.4, 16 x 1024 x 2048
+  // 4.6 : 8.0; but 16 x 5760 x 2880 10.4 : 9.1, 8 x 14336 x 4096 20.7 : 16.8, 16 x 4096 x 14336 22.2 : 17.4)
+  const int64_t codes = (int64_t)a.n * a.k;
+  const int row_ctas = cdiv(a.n, RW_N);
+  if (!a.offsets && (a.rows <= 8 ? codes <= 32 << 20 : a.rows <= RW_MAX_ROWS && codes <= 20 << 20 && row_ctas <= 2 * sms))
+    return {MatmulPlan::ROWS, 0, 1, row_ctas};
   // Groups: the sizes are not known here.  Up to 16 rows a group on average the narrow tiles read the matrices faster
   // (32 groups of 5760 x 2880: 64 rows 72.6 against 79.4, 256 rows 85.5 against 94.0); beyond, groups take more tiles than
   // one (1024 rows 114 against 103; 64 groups of 2816 x 2048, 2048 rows 84 against 71).
@@ -299,7 +304,8 @@ ts_moe_status ts_moe_fp8_matmul(const ts_moe_fp8_matmul_args* args, void* stream
   cudaError_t e;
   if (plan.kind == MatmulPlan::ROWS) {
     p.out_map = 0;
-    e = launch(fp8_row_kernel, dim3(plan.grid), RW_THREADS, 0, stream, p);
+    auto k = a.rows <= 8 ? fp8_row_kernel<1> : fp8_row_kernel<2>;
+    e = launch(k, dim3(plan.grid), RW_THREADS, 0, stream, p);
     return done(e, "fp8_matmul launch");
   }
   const bool tile = plan.kind == MatmulPlan::TILE;
