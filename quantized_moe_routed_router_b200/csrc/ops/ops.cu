@@ -88,7 +88,12 @@ ts_moe_status matmul_setup(const MatmulDevice** out) {
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return cuda_bad(e, "cudaGetDevice");
   if (dev < 0 || dev >= MAX_DEVICES) return set_last_error(TS_MOE_EUNSUPPORTED, "device ordinal >= 64");
-  std::lock_guard<std::mutex> lk(g_matmul_mu);
+  std::unique_lock<std::mutex> lk(g_matmul_mu, std::defer_lock);
+  try {
+    lk.lock();
+  } catch (...) {  // no exception leaves a C entry
+    return set_last_error(TS_MOE_ECUDA, "fp8_matmul: the set-up's lock failed");
+  }
   MatmulDevice& d = g_matmul[dev];
   if (!d.ready) {
     e = cudaDeviceGetAttribute(&d.sms, cudaDevAttrMultiProcessorCount, dev);

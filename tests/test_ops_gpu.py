@@ -1,5 +1,8 @@
 """The operators next to the routed half on the GPU, against their formulas in 64 bits (tests/ops_ref.py)."""
 import math
+import os
+import subprocess
+import sys
 
 import pytest
 import torch
@@ -707,3 +710,49 @@ def test_two_graphs_replayed_in_turn(B):
         for _, got, want, _ in cases:
             for x, y in zip(got, want):
                 assert torch.equal(x, y)
+
+
+FIRST_CALL = """
+import torch
+from quantized_moe_routed_router_b200 import binding as B
+from tests import ops_ref as R
+M, N, K, E = {M}, 2304, 512, 64
+g = torch.Generator(device="cuda")
+g.manual_seed(1)
+r = lambda *s: torch.randn(*s, generator=g, device="cuda")
+a, sa = R.encode_rows(r(M, K))
+b, sb = R.encode_matrix(r(N, K))
+x, l = r(M, N), r(M, E)
+idx = l.topk(4, -1).indices.to(torch.int32)
+out, y, q, s = torch.empty(M, N, device="cuda"), torch.empty(M, N, device="cuda"), R.rows8(M, N), torch.empty(M, N // 128, device="cuda")
+loss, counts, d = torch.empty(1, device="cuda"), torch.empty(E, dtype=torch.int32, device="cuda"), torch.empty_like(l)
+
+
+def run():
+    B.fp8_matmul(a, sa, b, sb, out)
+    B.rmsnorm(out, None, 1e-5, delta=x, y=y)
+    B.act_quant(y, x, 0, q, s)
+    B.balance(l, idx, 2, loss, counts, dlogits=d)
+    return out, y, q.view(torch.uint8), s, loss, counts, d
+
+
+torch.cuda.synchronize()
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    run()
+graph.replay()
+torch.cuda.synchronize()
+got = [t.clone() for t in (out, y, q.view(torch.uint8), s, loss, counts, d)]
+for t, u in zip(got, run()):
+    assert torch.equal(t, u)
+torch.cuda.synchronize()
+print("equal")
+"""
+
+
+@pytest.mark.parametrize("M", [4, 60, 3000])
+def test_first_call_of_a_process_is_captured(B, M):
+    """Nothing a first call sets up stands in the way of a capture."""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    p = subprocess.run([sys.executable, "-c", FIRST_CALL.format(M=M)], cwd=root, capture_output=True, text=True, timeout=120)
+    assert p.returncode == 0 and "equal" in p.stdout, p.stderr[-2000:]
