@@ -492,6 +492,7 @@ __global__ void __launch_bounds__(TL_THREADS, 1)
 
 // ----------------------------------------------------------------------------- few rows
 constexpr int ST_N = 128, ST_THREADS = 192;  // producer warp, MMA warp, 4 warps that scale and add
+constexpr int MAX_SPLITS = 4;                // CTAs of a cluster
 constexpr int ST_CHUNK = 8;                  // scale blocks whose row scales are staged at a time
 
 template <int BT>
@@ -544,24 +545,26 @@ __global__ void __launch_bounds__(ST_THREADS, StreamShape<BT>::CTAS)
   __syncthreads();
   tc_fence_after();
   cluster_sync();  // the peers' barriers are ready
+  // what needs no other kernel's results comes before the wait for them: divisions here took most of a microsecond
+  const uint32_t tmem = s.tmem;
+  const int nt = cdiv(p.a.n, ST_N);
+  const int c0 = p.kb * rank / splits, c1 = p.kb * (rank + 1) / splits;
+  const int first = blockIdx.x / splits, step = gridDim.x / splits;
+  const int t0 = first / nt, n00 = (first - t0 * nt) * ST_N;  // row tile and column of the first item
   grid_dep_wait();
   grid_dep_launch();
   if (p.a.offsets) {
     if (warp == 0) fill_groups(p.a, BT, s.groups);
     __syncthreads();
   }
-  const uint32_t tmem = s.tmem;
-  const int nt = cdiv(p.a.n, ST_N);
   const int items = s.groups.first[p.a.num_groups] * nt;
-  const int c0 = (int)((int64_t)p.kb * rank / splits), c1 = (int)((int64_t)p.kb * (rank + 1) / splits);
-  const int first = blockIdx.x / splits, step = gridDim.x / splits;
 
   if (warp == 0) {
     if (lane == 0) {
       unsigned it = 0;
       for (int t = first; t < items && !*dead; t += step) {
-        const int tt = t / nt, g = group_of(s.groups, p.a.num_groups, tt);
-        const int m0 = s.groups.lo[g] + (tt - s.groups.first[g]) * BT, n0 = (t - tt * nt) * ST_N;
+        const int tt = t == first ? t0 : t / nt, g = group_of(s.groups, p.a.num_groups, tt);
+        const int m0 = s.groups.lo[g] + (tt - s.groups.first[g]) * BT, n0 = t == first ? n00 : (t - tt * nt) * ST_N;
         for (int c = c0; c < c1; ++c, ++it) {
           const int st = it % S::STAGES;
           if (!wait_or_die(&s.empty[st], (it / S::STAGES & 1) ^ 1, dead)) break;
@@ -610,9 +613,9 @@ __global__ void __launch_bounds__(ST_THREADS, StreamShape<BT>::CTAS)
     const int type = p.a.out_type;
     unsigned it = 0, round = 0;
     for (int t = first; t < items; t += step, ++round) {
-      const int tt = t / nt, g = group_of(s.groups, p.a.num_groups, tt);
+      const int tt = t == first ? t0 : t / nt, g = group_of(s.groups, p.a.num_groups, tt);
       const int m0 = s.groups.lo[g] + (tt - s.groups.first[g]) * BT, rows = min(BT, s.groups.lo[g + 1] - m0);
-      const int n0 = (t - tt * nt) * ST_N;
+      const int n0 = t == first ? n00 : (t - tt * nt) * ST_N;
       const float* sb = p.a.b_scale + g * p.a.bs_group + (int64_t)(n0 / SCALE_BLOCK) * p.a.bs_row;
       float acc[BT], next[PER];
 #pragma unroll
@@ -682,24 +685,35 @@ __global__ void __launch_bounds__(ST_THREADS, StreamShape<BT>::CTAS)
       __syncwarp();
       const bool lost = *dead;
       const int j0 = rows * rank / splits, j1 = rows * (rank + 1) / splits;
-      // sixteen rows at a time: their loads run side by side
-      constexpr int R = 16;
+      // eight rows at a time of all CTAs: no load waits for another, nor for a branch (rows past the share are read and
+      // dropped; loads behind a condition each took 5500 cycles for six rows of three CTAs)
+      constexpr int R = 8;
+      const uint32_t mine_at = smem_addr(&s.red[0][r]);
+      uint32_t at[MAX_SPLITS];
+#pragma unroll
+      for (int q = 0; q < MAX_SPLITS; ++q) at[q] = peer_addr(mine_at, min(q, splits - 1));
       for (int jb = j0; jb < j1; jb += R) {
-        float v[R], d[R];
+        float w[MAX_SPLITS][R], d[R];
 #pragma unroll
-        for (int j = 0; j < R; ++j) {
-          const bool in = jb + j < j1 && n < p.a.n;
-          d[j] = p.a.add && in ? load1(p.a.add, type, (int64_t)(m0 + jb + j) * p.a.ld_add + n) : 0.f;
-          v[j] = 0.f;
-        }
-        for (int q = 0; q < splits; ++q) {
+        for (int q = 0; q < MAX_SPLITS; ++q) {
+          if (q < splits) {
 #pragma unroll
-          for (int j = 0; j < R; ++j)
-            if (jb + j < j1) v[j] += peer_load(peer_addr(smem_addr(&s.red[jb + j][r]), q));
+            for (int j = 0; j < R; ++j) w[q][j] = peer_load(at[q] + min(jb + j, BT - 1) * (uint32_t)(ST_N * sizeof(float)));
+          } else {
+#pragma unroll
+            for (int j = 0; j < R; ++j) w[q][j] = 0.f;
+          }
         }
 #pragma unroll
         for (int j = 0; j < R; ++j)
-          if (jb + j < j1 && n < p.a.n) store1(p.a.out, type, (int64_t)(m0 + jb + j) * p.a.ld_out + n, (lost ? NAN : v[j]) + d[j]);
+          d[j] = p.a.add && jb + j < j1 && n < p.a.n ? load1(p.a.add, type, (int64_t)(m0 + jb + j) * p.a.ld_add + n) : 0.f;
+#pragma unroll
+        for (int j = 0; j < R; ++j) {
+          float v = w[0][j];
+#pragma unroll
+          for (int q = 1; q < MAX_SPLITS; ++q) v += w[q][j];
+          if (jb + j < j1 && n < p.a.n) store1(p.a.out, type, (int64_t)(m0 + jb + j) * p.a.ld_out + n, (lost ? NAN : v) + d[j]);
+        }
       }
       __syncwarp();
       if (lane < splits) peer_arrive(peer_addr(smem_addr(&s.red_free), lane));

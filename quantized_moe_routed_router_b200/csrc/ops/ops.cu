@@ -173,7 +173,7 @@ MatmulPlan matmul_plan(const ts_moe_fp8_matmul_args& a, int sms) {
   const int64_t items = (cdiv(a.rows, bt) + reached - 1) * cdiv(a.n, ST_N);
   // K is split while that leaves one CTA an SM, or two where one would leave K whole, never into a second wave: a cluster
   // joins its shares in some 1 to 2 us (64 x 4096 x 4096: whole 14.8, 2 ways 11.5, 4 ways 11.4, 8 ways 25.0).
-  const int splits = (int)std::max<int64_t>(1, std::min<int64_t>(std::min(4, kb), (items * 2 <= sms ? sms : 2 * sms) / items));
+  const int splits = (int)std::max<int64_t>(1, std::min<int64_t>(std::min(MAX_SPLITS, kb), (items * 2 <= sms ? sms : 2 * sms) / items));
   const MatmulPlan stream = {MatmulPlan::STREAM, bt, splits, (int)std::min<int64_t>(items, 2 * sms / splits)};
   if (G > 1) return stream;
   // One matrix: what each would take, by 0.5 a block of K and tile against a fixed 7.5 and the larger of 0.13 a block in
