@@ -103,6 +103,36 @@ TSM_DEV void store1(void* p, int type, int64_t i, float v) {
     ((__half*)p)[i] = __float2half_rn(v);
 }
 
+// Column n of rows m0 .. m0 + count - 1 (count <= R; past it the last row again): the loads go out one after another, with
+// no branch between them.
+template <int R>
+TSM_DEV void load_column(const void* base, int type, int64_t ld, int64_t m0, int count, int64_t n, float (&v)[R]) {
+  const int64_t at = m0 * ld + n;
+  if (type == TS_DT_FP32) {
+#pragma unroll
+    for (int j = 0; j < R; ++j) v[j] = ((const float*)base)[at + min(j, count - 1) * ld];
+  } else {
+    uint16_t w[R];
+#pragma unroll
+    for (int j = 0; j < R; ++j) w[j] = ((const uint16_t*)base)[at + min(j, count - 1) * ld];
+#pragma unroll
+    for (int j = 0; j < R; ++j) v[j] = type == TS_DT_BF16 ? __uint_as_float((uint32_t)w[j] << 16) : __half2float(__ushort_as_half(w[j]));
+  }
+}
+template <int R>
+TSM_DEV void store_column(void* base, int type, int64_t ld, int64_t m0, int count, int64_t n, const float (&v)[R]) {
+  const int64_t at = m0 * ld + n;
+  if (type == TS_DT_FP32) {
+#pragma unroll
+    for (int j = 0; j < R; ++j)
+      if (j < count) ((float*)base)[at + j * ld] = v[j];
+  } else {
+#pragma unroll
+    for (int j = 0; j < R; ++j)
+      if (j < count) ((uint16_t*)base)[at + j * ld] = (uint16_t)pack2(v[j], 0.f, type);
+  }
+}
+
 // ----------------------------------------------------------------------------- many rows
 constexpr int TL_M = 128, TL_N = 256, TL_STAGES = 3, TL_ACC = 2;  // TL_ACC x TL_N = all 512 columns of tensor memory
 constexpr int TL_BAND = 16;     // row tiles that run side by side over the columns: their rows of A stay in L2
@@ -314,7 +344,7 @@ TSM_DEV void store_tile(const MatmulParams& p, const CUtensorMap* mo, float (&ac
 // Persistent, a tile at a time; the MMAs of a tile's first blocks run while the last one is stored.  Per block of K the
 // MMAs of 128 x 256 take 512 cycles at the tensor pipe's peak, and so does nothing else alone; what bounds the kernel is
 // the chain from the MMAs' end over the read-back to the next MMAs in the same half of tensor memory, and the chip's
-// power: 8192 x 14336 x 4096 in 479 us (2.0 PFLOP/s, tensor pipe 52 %), 312 us with the sums taken out.  128 rows, not
+// power: 8192 x 14336 x 4096 in 476 us (2.0 PFLOP/s, tensor pipe 52 %), 312 us with the sums taken out.  128 rows, not
 // 256: groups waste half a tile on average.
 __global__ void __launch_bounds__(TL_THREADS, 1)
     fp8_tile_kernel(const __grid_constant__ MatmulParams p, const __grid_constant__ CUtensorMap ma,
@@ -517,7 +547,7 @@ struct StreamSmem {
 };
 
 // The matrix as the MMA's first operand: 128 of its rows are one instruction's, whatever few tokens there are.  64 routes
-// over 32 experts of 5760 x 2880 in 77.5 us (6.0 TB/s: HBM bounds it); 16 x 5760 x 2880 in 9.1 us, of which 2.6 us are
+// over 32 experts of 5760 x 2880 in 75.8 us (6.1 TB/s: HBM bounds it); 16 x 5760 x 2880 in 6.7 us, of which 2.6 us are
 // traffic and the rest a chain of latencies (launch, TMA, MMA, read-back, the cluster's sum).
 template <int BT>
 __global__ void __launch_bounds__(ST_THREADS, StreamShape<BT>::CTAS)
@@ -664,14 +694,13 @@ __global__ void __launch_bounds__(ST_THREADS, StreamShape<BT>::CTAS)
         const bool lost = *dead;
 #pragma unroll
         for (int j0 = 0; j0 < BT; j0 += 8) {
-          float d[8];
+          if (j0 < rows && n < p.a.n) {
+            float v[8], d[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+            if (p.a.add) load_column<8>(p.a.add, type, p.a.ld_add, m0 + j0, min(rows - j0, 8), n, d);
 #pragma unroll
-          for (int j = 0; j < 8; ++j)
-            d[j] = p.a.add && j0 + j < rows && n < p.a.n ? load1(p.a.add, type, (int64_t)(m0 + j0 + j) * p.a.ld_add + n) : 0.f;
-#pragma unroll
-          for (int j = 0; j < 8; ++j)
-            if (j0 + j < rows && n < p.a.n)
-              store1(p.a.out, type, (int64_t)(m0 + j0 + j) * p.a.ld_out + n, (lost ? NAN : acc[j0 + j]) + d[j]);
+            for (int j = 0; j < 8; ++j) v[j] = (lost ? NAN : acc[j0 + j]) + d[j];
+            store_column<8>(p.a.out, type, p.a.ld_out, m0 + j0, min(rows - j0, 8), n, v);
+          }
         }
         continue;
       }
@@ -693,7 +722,7 @@ __global__ void __launch_bounds__(ST_THREADS, StreamShape<BT>::CTAS)
 #pragma unroll
       for (int q = 0; q < MAX_SPLITS; ++q) at[q] = peer_addr(mine_at, min(q, splits - 1));
       for (int jb = j0; jb < j1; jb += R) {
-        float w[MAX_SPLITS][R], d[R];
+        float w[MAX_SPLITS][R], d[R] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int q = 0; q < MAX_SPLITS; ++q) {
           if (q < splits) {
@@ -704,15 +733,16 @@ __global__ void __launch_bounds__(ST_THREADS, StreamShape<BT>::CTAS)
             for (int j = 0; j < R; ++j) w[q][j] = 0.f;
           }
         }
+if (n < p.a.n) {
+          if (p.a.add) load_column<R>(p.a.add, type, p.a.ld_add, m0 + jb, min(j1 - jb, R), n, d);
 #pragma unroll
-        for (int j = 0; j < R; ++j)
-          d[j] = p.a.add && jb + j < j1 && n < p.a.n ? load1(p.a.add, type, (int64_t)(m0 + jb + j) * p.a.ld_add + n) : 0.f;
+          for (int j = 0; j < R; ++j) {
+            float v = w[0][j];
 #pragma unroll
-        for (int j = 0; j < R; ++j) {
-          float v = w[0][j];
-#pragma unroll
-          for (int q = 1; q < MAX_SPLITS; ++q) v += w[q][j];
-          if (jb + j < j1 && n < p.a.n) store1(p.a.out, type, (int64_t)(m0 + jb + j) * p.a.ld_out + n, (lost ? NAN : v) + d[j]);
+            for (int q = 1; q < MAX_SPLITS; ++q) v += w[q][j];
+            d[j] += lost ? NAN : v;
+          }
+          store_column<R>(p.a.out, type, p.a.ld_out, m0 + jb, min(j1 - jb, R), n, d);
         }
       }
       __syncwarp();
@@ -729,7 +759,8 @@ __global__ void __launch_bounds__(ST_THREADS, StreamShape<BT>::CTAS)
 // mma.sync m16n8k16 in FP16 (every E4M3 code is an FP16 value, products and sums in float32): the matrix's rows are the
 // MMA's, tokens its columns.  Which k stands at which place of a fragment is free as long as both operands agree, so a
 // lane takes sixteen neighbouring codes of a row and they serve four MMAs.  Registers, one barrier and no other
-// set-up: at 16 x 1024 x 2048 fp8_stream_kernel takes 8.2 us of which 0.3 us are traffic.
+// set-up: 1 x 1024 x 2048 in 3.4 us against 5.3 by fp8_stream_kernel, 1 x 4096 x 4096 in 6.2 us (2.7 TB/s); the launch and
+// the trips to HBM of a warp's few blocks one after another bound it.
 constexpr int RW_N = 16, RW_MAX_ROWS = 16, RW_WARPS = 8, RW_THREADS = 32 * RW_WARPS;
 
 // Sixteen codes from `at` of a row of k; past k they are zeros.

@@ -158,12 +158,11 @@ MatmulPlan matmul_plan(const ts_moe_fp8_matmul_args& a, int sms) {
   const int64_t mean = cdiv(a.rows, (int)reached);
   const int64_t tiles = (cdiv(a.rows, TL_M) + reached - 1) * cdiv(a.n, TL_N);
   const MatmulPlan tile = {MatmulPlan::TILE, 0, 1, (int)std::min<int64_t>(tiles, sms)};
-  // A decode step: without set-up, while the matrix is small enough for that to count and the CTAs run at once (against
-  // fp8_stream_kernel: 1 x 4096 x 4096 6.2 : 8.8, 8 x 5760 x 2880 8.1 : 8.9, 16 x 4096 x 4096 8.2 : 9.4, 16 x 1024 x 2048
-  // 4.6 : 8.0; but 16 x 5760 x 2880 10.4 : 9.1, 8 x 14336 x 4096 20.7 : 16.8, 16 x 4096 x 14336 22.2 : 17.4)
-  const int64_t codes = (int64_t)a.n * a.k;
+  // A decode step: without set-up, while the CTAs run at once and a warp's share of K is a few blocks (against
+  // fp8_stream_kernel: 1 x 1024 x 2048 3.4 : 5.3, 4 x 2880 x 2880 4.9 : 6.1, 1 x 4096 x 4096 6.2 : 6.4, 16 x 1024 x 2048
+  // 4.6 : 5.6; but 8 x 5760 x 2880 8.0 : 6.7, 1 x 2048 x 8192 8.7 : 8.2, 16 x 2048 x 4096 7.0 : 6.6)
   const int row_ctas = cdiv(a.n, RW_N);
-  if (!a.offsets && (a.rows <= 8 ? codes <= 32 << 20 : a.rows <= RW_MAX_ROWS && codes <= 20 << 20 && row_ctas <= 2 * sms))
+  if (!a.offsets && a.rows <= RW_MAX_ROWS && row_ctas <= 2 * sms && kb <= (a.rows <= 8 ? 32 : 16))
     return {MatmulPlan::ROWS, 0, 1, row_ctas};
   // Groups: the sizes are not known here.  Up to 16 rows a group on average the narrow tiles read the matrices faster
   // (32 groups of 5760 x 2880: 64 rows 72.6 against 79.4, 256 rows 85.5 against 94.0); beyond, groups take more tiles than
@@ -172,16 +171,18 @@ MatmulPlan matmul_plan(const ts_moe_fp8_matmul_args& a, int sms) {
   const int bt = mean <= 16 ? 16 : 32;
   const int64_t items = (cdiv(a.rows, bt) + reached - 1) * cdiv(a.n, ST_N);
   // K is split while that leaves one CTA an SM, or two where one would leave K whole, never into a second wave: a cluster
-  // joins its shares in some 1 to 2 us (64 x 4096 x 4096: whole 14.8, 2 ways 11.5, 4 ways 11.4, 8 ways 25.0).
+  // joins its shares in about a microsecond, at every item (64 x 4096 x 4096, with an earlier, slower join: whole 14.8,
+  // 2 ways 11.5, 4 ways 11.4, 8 ways 25.0).
   const int splits = (int)std::max<int64_t>(1, std::min<int64_t>(std::min(MAX_SPLITS, kb), (items * 2 <= sms ? sms : 2 * sms) / items));
   const MatmulPlan stream = {MatmulPlan::STREAM, bt, splits, (int)std::min<int64_t>(items, 2 * sms / splits)};
   if (G > 1) return stream;
-  // One matrix: what each would take, by 0.5 a block of K and tile against a fixed 7.5 and the larger of 0.13 a block in
-  // sequence and the traffic from L2 at 8 TB/s (128 x 4096 x 4096: 20.1 against 13.6; 128 x 14336 x 4096: 22.7 against 36.7).
-  // Tiles wait for what they add, and shift rows at odd places (333 x 2047 x 1408: 10.4 plain, 13.1 odd, 24.2 odd with add).
+  // One matrix: what each would take, by 0.5 a block of K and tile against a fixed 5 and the larger of 0.13 a block in
+  // sequence and the traffic from L2 at 8 TB/s (tile : stream: 128 x 2880 x 2880 16.1 : 9.8, 333 x 2048 x 1408 10.7 : 7.6,
+  // 600 x 1024 x 1024 9.2 : 6.4, 256 x 4096 x 1024 9.2 : 9.2, 128 x 14336 x 4096 22.7 : 36.7).  Tiles wait for what they
+  // add, and shift rows at odd places.
   const double rest = (a.add ? 5.0 : 0.0) + (aligned(a.out, a.ld_out * dt_size(a.out_type), 16) ? 0.0 : 3.0);
   const double t_tile = 4.0 + (double)((tiles + sms - 1) / sms) * (1.5 + 0.5 * kb + rest);
-  const double t_stream = 7.5 + std::max(0.13 * (double)((items * splits + 2 * sms - 1) / (2 * sms)) * cdiv(kb, splits),
+  const double t_stream = 5.0 + std::max(0.13 * (double)((items * splits + 2 * sms - 1) / (2 * sms)) * cdiv(kb, splits),
                                          (double)items * kb * (SCALE_BLOCK * (ST_N + bt)) / 8e6);
   return t_tile <= t_stream ? tile : stream;
 }
