@@ -148,7 +148,7 @@ TSM_DEV void balance_quad(const uint32_t (&q)[WIDE ? 4 : 2], int type, float (&v
 }
 
 // SIGMOID: the score.  WIDE: logits and their gradient in 32 bits.
-// 65536 x 256 sigmoid with the gradient: 46 us with the counting launch (134 MB, floor 20.8); issue slots bound the pass
+// 65536 x 256 sigmoid with the gradient: 45 us with the counting launch (134 MB, floor 20.8); issue slots bound the pass
 // over the logits (69 % busy, some 40 instructions a logit).
 template <int LPR, int NV, bool SIGMOID, bool WIDE>
 __global__ void __launch_bounds__(BAL_THREADS) balance_kernel(const BalanceParams p) {
@@ -173,7 +173,7 @@ __global__ void __launch_bounds__(BAL_THREADS) balance_kernel(const BalanceParam
     // whole numbers: the order of the additions does not change the counts
     const int segs = (int)blockDim.x / BAL_MAX_E, e = tid % BAL_MAX_E;
     int sum = 0;
-#pragma unroll 8
+#pragma unroll 16
     for (int b = tid / BAL_MAX_E; b < p.count_ctas; b += segs) sum += p.head->counts[b][e];
     if (sum) atomicAdd(&hist[e], sum);
     if (tid < p.count_ctas) atomicAdd(&hist[BAL_MAX_E], p.head->counts[tid][BAL_MAX_E]);
@@ -275,7 +275,7 @@ __global__ void __launch_bounds__(BAL_THREADS) balance_kernel(const BalanceParam
       }
       reduce();
     }
-    const float inv = !on || s == 0.f ? 0.f : 1.f / s;
+    const float inv = !on || s == 0.f ? 0.f : rcp(s);  // s is 0 or in the normal range: at least 0.25 or one term near 1
     fp *= inv;
     const float c = on ? gscale * inv : 0.f;
 #pragma unroll
@@ -341,7 +341,7 @@ __global__ void __launch_bounds__(BAL_THREADS) balance_kernel(const BalanceParam
     const int segs = (int)blockDim.x / BAL_MAX_E, seg = tid / BAL_MAX_E, e = tid % BAL_MAX_E;
     float part = 0.f;
     if (e < E) {
-#pragma unroll 8
+#pragma unroll 16
       for (int b = seg; b < (int)gridDim.x; b += segs) part += __ldcg(&p.part[(int64_t)b * E + e]);
     }
     sums[seg][e] = part;
