@@ -31,8 +31,8 @@ TSM_DEV void act8(const ts_moe_act_quant_args& a, const float (&g)[8], const flo
 
 // A warp takes four neighbouring groups of a row, eight lanes and two chunks of eight columns a lane each; quads
 // row-major.  step_rows, step_quads: the grid's warps as whole rows of quads and the rest, so that the loop divides
-// nothing.  With VEC the next quad's loads are issued before this one is worked on: 8192 x 14336 bf16 in 94.5 us
-// (6.3 TB/s, HBM bounds it); without, and with 16 lanes a group and IEEE divisions, 162 us.
+// nothing.  With VEC the next quad's loads are issued before this one is worked on: 8192 x 14336 bf16 in 96 us
+// (6.1 TB/s, HBM bounds it); without, and with 16 lanes a group and IEEE divisions, 162 us.
 template <bool VEC, bool WIDE>
 __global__ void __launch_bounds__(ACT_THREADS, VEC && WIDE ? 2 : 4)
     act_quant_kernel(const ts_moe_act_quant_args a, int quads, int step_rows, int step_quads) {

@@ -1,6 +1,7 @@
 // Element access shared by the operators: eight consecutive elements of a
 // 16- or 32-bit row as float32, and groups of 128 columns as E4M3.
 #pragma once
+#include <cfloat>
 #include <cuda_fp8.h>
 
 #include "../../../include/ts_moe_ops.h"
@@ -205,15 +206,45 @@ TSM_DEV float min_nan(float a, float b) {
   return r;
 }
 
+// a / b rounded, from r, the rounded 1 / b: one FMA forms what the first quotient leaves of a, exactly while nothing in it
+// is subnormal, and another adds its share (Markstein, IBM Journal of Research and Development 34, 1990).
+TSM_DEV float quotient(float a, float b, float r) {
+  const float q = a * r;
+  return fmaf(fmaf(-q, b, a), r, q);
+}
+
+// Two values to an instruction.
+TSM_DEV uint64_t pair(float x, float y) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
+  return r;
+}
+TSM_DEV float2 unpair(uint64_t x) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(x));
+  return r;
+}
+TSM_DEV uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+TSM_DEV uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+
 // LANES neighbouring lanes hold the 128 columns of one group in chunks of eight
 // columns: chunk c of lane l stands at column (c LANES + l) 8 of the group (lanes
 // past the row's end hold zeros).  Writes the group's E4M3 codes and, from its
-// first lane, its scale.  amax / 448 is formed as a product with the rounded
-// reciprocal and the codes as products with rcp(scale), each within 2 ulp of the
-// quotient, which moves a code only where v / scale lies that close to the middle
-// between two codes; IEEE divisions here cost as many instructions as the eight
-// values of a lane.  The conversion saturates, so the group's largest value lands
-// on 448 whichever way that rounds.
+// first lane, its scale.  Both are rounded quotients: with 16-bit inputs some
+// values in a thousand stand exactly between two codes, and a product with an
+// approximate reciprocal put a tenth of those on the other one.  A group's values
+// share the reciprocal, so a quotient costs two FMAs more than a product, and two
+// values share an instruction.  The
+// conversion saturates, so the group's largest value lands on 448 whichever way
+// it rounds.
 template <int LANES, bool VEC>
 TSM_DEV void quant_group(const float (&v)[16 / LANES][8], uint8_t* q, int64_t off, int n, float* scale) {
   constexpr int C = 16 / LANES;
@@ -225,17 +256,35 @@ TSM_DEV void quant_group(const float (&v)[16 / LANES][8], uint8_t* q, int64_t of
   }
 #pragma unroll
   for (int d = LANES / 2; d >= 1; d >>= 1) m = max_nan(m, __shfl_xor_sync(0xFFFFFFFFu, m, d, LANES));
-  const float s = m * (1.f / E4M3_MAX);
-  const float inv = rcp(s);
+  const float s = m <= FLT_MAX ? quotient(m, E4M3_MAX, 1.f / E4M3_MAX) : m;
+  // A tiny group is taken times 2^64, which keeps the remainders out of the subnormal range; for an infinite scale they are
+  // left out (0 and NaN stay what they are).  The reciprocal is rounded by the same step from the approximate one.
+  const bool tiny = s < 0x1p-60f;
+  const float b = tiny ? s * 0x1p64f : s, rest = b <= FLT_MAX ? -b : 0.f, r0 = rcp(b), inv = fmaf(fmaf(rest, r0, 1.f), r0, r0);
+  uint64_t t[C][4];
 #pragma unroll
   for (int c = 0; c < C; ++c) {
-    uint32_t w[2];
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(v[c][4 * j] * inv, v[c][4 * j + 1] * inv), __NV_SATFINITE, __NV_E4M3);
-      const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(v[c][4 * j + 2] * inv, v[c][4 * j + 3] * inv), __NV_SATFINITE, __NV_E4M3);
-      w[j] = lo | hi << 16;
+    for (int j = 0; j < 4; ++j) t[c][j] = pair(v[c][2 * j], v[c][2 * j + 1]);
+  }
+  if (tiny) {
+    const uint64_t up = pair(0x1p64f, 0x1p64f);
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) t[c][j] = mul2(t[c][j], up);
     }
+  }
+  const uint64_t inv2 = pair(inv, inv), rest2 = pair(rest, rest);
+#pragma unroll
+  for (int c = 0; c < C; ++c) {
+    uint32_t h[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {  // quotient(), two values at a time
+      const uint64_t q0 = mul2(t[c][j], inv2);
+      h[j] = __nv_cvt_float2_to_fp8x2(unpair(fma2(fma2(q0, rest2, t[c][j]), inv2, q0)), __NV_SATFINITE, __NV_E4M3);
+    }
+    const uint32_t w[2] = {h[0] | h[1] << 16, h[2] | h[3] << 16};
     const int64_t at = off + c * LANES * 8;
     const int nc = n - c * LANES * 8;
     if (VEC) {

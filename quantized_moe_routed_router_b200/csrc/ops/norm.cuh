@@ -5,7 +5,7 @@
 //
 // One pass: a CTA holds its row in registers between the sum of squares and the
 // outputs, so every byte is read and written once and HBM bounds the kernel:
-// 16384 x 4096 bf16, with the sum, y and q, 98.7 us (6.1 TB/s); walking the rows
+// 16384 x 4096 bf16, with the sum, y and q, 100.7 us (6.0 TB/s); walking the rows
 // with the next one's loads in flight took it there from 180 us at a CTA a row.
 #pragma once
 #include "elem.cuh"
