@@ -1,9 +1,10 @@
 /*
- * ts_moe_debug.h -- helpers exported for tests.  All but the last expose the
+ * ts_moe_debug.h -- helpers exported for tests.  All but the last two expose the
  * pure arithmetic the kernels use to split work between CTAs and the open-time
  * validation, so both can be checked on a machine without a GPU; they touch
- * neither device memory nor the CUDA runtime.  The last one changes a
- * handle's device counters so that a test can make a bounded wait run out.
+ * neither device memory nor the CUDA runtime.  The last two let a test make a
+ * bounded wait run out: one changes a handle's device counters, one runs a
+ * product in which a CTA waits for copies that it never issues.
  */
 #ifndef TS_MOE_DEBUG_H
 #define TS_MOE_DEBUG_H
@@ -11,6 +12,7 @@
 #include <stdint.h>
 
 #include "ts_moe.h"
+#include "ts_moe_ops.h"
 
 #ifdef __cplusplus
 extern "C" {
@@ -48,6 +50,13 @@ ts_moe_status ts_moe_debug_validate(const ts_moe_config* cfg, const ts_moe_layer
  * returns TS_MOE_EDEVICE and re-zeroes the counters, after which calls work
  * normally again.  Not for production use. */
 ts_moe_status ts_moe_debug_skew_barrier(ts_moe* h, void* stream);
+
+/* Failure-path test hook.  ts_moe_fp8_matmul in which CTA `cta` issues no
+ * copies, and so gives up its waits after `wait_us` (at most 2 s) each; the
+ * other CTAs keep their limit.  The kernel runs to its end, and the outputs
+ * that need that CTA's sums are NaN.  Refused where the call takes the kernel
+ * without waits.  Not for production use. */
+ts_moe_status ts_moe_debug_fp8_matmul_held(const ts_moe_fp8_matmul_args* args, int cta, uint32_t wait_us, void* stream);
 
 #ifdef __cplusplus
 }

@@ -116,13 +116,14 @@ def _load():
     lib.ts_moe_rmsnorm.argtypes = [C.POINTER(RmsnormArgs), vp]
     lib.ts_moe_act_quant.argtypes = [C.POINTER(ActQuantArgs), vp]
     lib.ts_moe_fp8_matmul.argtypes = [C.POINTER(Fp8MatmulArgs), vp]
+    lib.ts_moe_debug_fp8_matmul_held.argtypes = [C.POINTER(Fp8MatmulArgs), i32, C.c_uint32, vp]
     lib.ts_moe_balance.argtypes = [C.POINTER(BalanceArgs), vp]
     lib.ts_moe_balance_workspace.argtypes = [C.c_int32, C.c_int32]
     lib.ts_moe_balance_workspace.restype = C.c_uint64
     for f in ("ts_moe_open", "ts_moe_route", "ts_moe_forward", "ts_moe_device_status", "ts_moe_get_info",
               "ts_moe_set_timing_events", "ts_moe_close", "ts_moe_debug_validate", "ts_moe_route_noalloc",
               "ts_moe_debug_skew_barrier", "ts_moe_rmsnorm", "ts_moe_act_quant", "ts_moe_fp8_matmul",
-              "ts_moe_balance"):
+              "ts_moe_balance", "ts_moe_debug_fp8_matmul_held"):
         getattr(lib, f).restype = C.c_int
     return lib
 

@@ -33,8 +33,7 @@ def sources() -> list:
 def units() -> list:
     """(source, object, files it is built from) of each translation unit."""
     base = _files(CSRC, INCLUDE)
-    handle = [p for p in base if os.path.basename(p) != "ts_moe_ops.h"]   # the routed half does not include it
-    return [(os.path.join(CSRC, "ts_moe.cu"), os.path.join(OBJ, "ts_moe.o"), handle),
+    return [(os.path.join(CSRC, "ts_moe.cu"), os.path.join(OBJ, "ts_moe.o"), base),
             (os.path.join(OPS, "ops.cu"), os.path.join(OBJ, "ops.o"), base + _files(OPS))]
 
 

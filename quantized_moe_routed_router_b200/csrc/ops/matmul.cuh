@@ -25,6 +25,8 @@ struct MatmulParams {
   int kb;      // scale blocks of K
   int splits;  // fp8_stream_kernel: CTAs of a cluster, which share K
   int out_map; // fp8_tile_kernel: out has a tensor map (rows from 16-byte boundary to 16-byte boundary)
+  int held;    // a CTA that issues no copies and waits held_us at most: the failure path, for tests; -1: none
+  unsigned held_us;
 };
 
 // ----------------------------------------------------------------------------- groups
@@ -150,7 +152,7 @@ struct TileSmem {
   float scale[2][TL_CHUNK][TL_N / SCALE_BLOCK][TL_M];  // products of the scales, TL_CHUNK blocks at a time
   uint64_t full[TL_STAGES], empty[TL_STAGES], acc_full[TL_ACC], acc_empty[TL_ACC], sc_full[2], sc_empty[2], drain;
   uint32_t tmem;
-  int dead;
+  DeadMark dead;
   GroupTable groups;
 };
 
@@ -354,13 +356,14 @@ __global__ void __launch_bounds__(TL_THREADS, 1)
   extern __shared__ uint8_t raw[];
   TileSmem& s = *reinterpret_cast<TileSmem*>(raw);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  volatile int* dead = &s.dead;
+  const Dead dead = {&s.dead};
   if (threadIdx.x == 0) {
     for (int i = 0; i < TL_STAGES; ++i) mbar_init(&s.full[i], 1), mbar_init(&s.empty[i], 1);
     for (int i = 0; i < TL_ACC; ++i) mbar_init(&s.acc_full[i], 1), mbar_init(&s.acc_empty[i], TL_ADDERS);
     for (int i = 0; i < 2; ++i) mbar_init(&s.sc_full[i], 64), mbar_init(&s.sc_empty[i], TL_ADDERS);
     mbar_init(&s.drain, 1);
-    s.dead = (smem_addr(raw) & 1023) != 0;
+    s.dead.set = (smem_addr(raw) & 1023) != 0;
+    s.dead.limit_us = (int)blockIdx.x == p.held ? p.held_us : WAIT_LIMIT_US;
     fence_barrier_init();
     prefetch_map(&ma);
     prefetch_map(&mb);
@@ -379,22 +382,21 @@ __global__ void __launch_bounds__(TL_THREADS, 1)
   if (warp == 0) {
     if (lane == 0) {
       unsigned it = 0;
-      for (int t = blockIdx.x; t < tiles && !*dead; t += gridDim.x) {
+      for (int t = blockIdx.x; t < tiles && !dead; t += gridDim.x) {
         const Tile tl = locate_tile(p, s.groups, t);
         for (int c = 0; c < p.kb; ++c, ++it) {
           const int st = it % TL_STAGES;
           if (!wait_or_die(&s.empty[st], (it / TL_STAGES & 1) ^ 1, dead)) break;
+          if ((int)blockIdx.x == p.held) continue;
           mbar_arrive_expect_tx(&s.full[st], (TL_M + TL_N) * SCALE_BLOCK);
           tma_load_2d(s.a[st], &ma, c * SCALE_BLOCK, tl.m0, &s.full[st]);
           tma_load_3d(s.b[st], &mb, c * SCALE_BLOCK, tl.n0, tl.g, &s.full[st]);
         }
       }
       // no copy may be in flight when the CTA ends
-      if (*dead) {
+      if (dead) {
         for (unsigned i = it > TL_STAGES ? it - TL_STAGES : 0; i < it; ++i) {
-          const unsigned long long t0 = globaltimer();
-          while (!mbar_try_wait(&s.full[i % TL_STAGES], i / TL_STAGES & 1) && globaltimer() - t0 < WAIT_LIMIT_NS) {
-          }
+          wait_at_end(&s.full[i % TL_STAGES], i / TL_STAGES & 1, dead);
         }
       }
     }
@@ -405,7 +407,7 @@ __global__ void __launch_bounds__(TL_THREADS, 1)
     constexpr uint32_t idesc = umma_idesc(TL_M, TL_N);
     const uint64_t da0 = umma_desc(smem_addr(s.a[0])), db0 = umma_desc(smem_addr(s.b[0]));
     unsigned it = 0;
-    for (int t = blockIdx.x; t < tiles && !*dead; t += gridDim.x) {
+    for (int t = blockIdx.x; t < tiles && !dead; t += gridDim.x) {
       for (int c = 0; c < p.kb; ++c, ++it) {
         const int st = it % TL_STAGES, ac = it % TL_ACC;
         const bool ok = wait_both_or_die(&s.acc_empty[ac], (it / TL_ACC & 1) ^ 1, &s.full[st], it / TL_STAGES & 1, dead);
@@ -423,15 +425,13 @@ __global__ void __launch_bounds__(TL_THREADS, 1)
     }
     // no MMA may be in flight when tensor memory is freed
     if (elect_one()) umma_commit(&s.drain);
-    const unsigned long long t0 = globaltimer();
-    while (!mbar_try_wait(&s.drain, 0) && globaltimer() - t0 < WAIT_LIMIT_NS) {
-    }
+    wait_at_end(&s.drain, 0, dead);
   } else if (warp < 4) {
     // the scales: thread i those of the tile's rows i and i + 64, times the column blocks'
     const int r = threadIdx.x - 64, nblocks = cdiv(p.a.n, SCALE_BLOCK);
     const bool vec = p.a.as_block == 1 && ((uintptr_t)p.a.a_scale | (uintptr_t)(p.a.as_row * 4)) % 16 == 0;
     unsigned it = 0;
-    for (int t = blockIdx.x; t < tiles && !*dead; t += gridDim.x) {
+    for (int t = blockIdx.x; t < tiles && !dead; t += gridDim.x) {
       const Tile tl = locate_tile(p, s.groups, t);
       const float* sb = p.a.b_scale + tl.g * p.a.bs_group;
       const int64_t b0 = (int64_t)(tl.n0 / SCALE_BLOCK) * p.a.bs_row, b1 = (int64_t)min(tl.n0 / SCALE_BLOCK + 1, nblocks - 1) * p.a.bs_row;
@@ -506,7 +506,7 @@ __global__ void __launch_bounds__(TL_THREADS, 1)
           }
         }
       }
-      if (*dead) {
+      if (dead) {
 #pragma unroll
         for (int j = 0; j < TL_COLS; ++j) acc[j] = NAN;
       }
@@ -542,7 +542,7 @@ struct StreamSmem {
   float scale[2][ST_CHUNK][BT];     // sa * sb of the blocks at hand
   uint64_t full[S::STAGES], empty[S::STAGES], acc_full[S::ACC], acc_empty[S::ACC], red_full, red_free, drain;
   uint32_t tmem;
-  int dead;
+  DeadMark dead;
   GroupTable groups;
 };
 
@@ -556,7 +556,7 @@ __global__ void __launch_bounds__(ST_THREADS, StreamShape<BT>::CTAS)
   extern __shared__ uint8_t raw[];
   StreamSmem<BT>& s = *reinterpret_cast<StreamSmem<BT>*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  volatile int* dead = &s.dead;
+  const Dead dead = {&s.dead};
   const int splits = p.splits, rank = (int)cluster_rank();
   if (threadIdx.x == 0) {
     for (int i = 0; i < S::STAGES; ++i) mbar_init(&s.full[i], 1), mbar_init(&s.empty[i], 1);
@@ -564,7 +564,8 @@ __global__ void __launch_bounds__(ST_THREADS, StreamShape<BT>::CTAS)
     mbar_init(&s.red_full, 4 * splits);
     mbar_init(&s.red_free, 4 * splits);
     mbar_init(&s.drain, 1);
-    s.dead = 0;
+    s.dead.set = 0;
+    s.dead.limit_us = (int)blockIdx.x == p.held ? p.held_us : WAIT_LIMIT_US;
     fence_barrier_init();
     prefetch_map(&ma);
     prefetch_map(&mb);
@@ -592,22 +593,21 @@ __global__ void __launch_bounds__(ST_THREADS, StreamShape<BT>::CTAS)
   if (warp == 0) {
     if (lane == 0) {
       unsigned it = 0;
-      for (int t = first; t < items && !*dead; t += step) {
+      for (int t = first; t < items && !dead; t += step) {
         const int tt = t == first ? t0 : t / nt, g = group_of(s.groups, p.a.num_groups, tt);
         const int m0 = s.groups.lo[g] + (tt - s.groups.first[g]) * BT, n0 = t == first ? n00 : (t - tt * nt) * ST_N;
         for (int c = c0; c < c1; ++c, ++it) {
           const int st = it % S::STAGES;
           if (!wait_or_die(&s.empty[st], (it / S::STAGES & 1) ^ 1, dead)) break;
+          if ((int)blockIdx.x == p.held) continue;
           mbar_arrive_expect_tx(&s.full[st], (ST_N + BT) * SCALE_BLOCK);
           tma_load_3d(s.b[st], &mb, c * SCALE_BLOCK, n0, g, &s.full[st]);
           tma_load_2d(s.a[st], &ma, c * SCALE_BLOCK, m0, &s.full[st]);
         }
       }
-      if (*dead) {
+      if (dead) {
         for (unsigned i = it > S::STAGES ? it - S::STAGES : 0; i < it; ++i) {
-          const unsigned long long t0 = globaltimer();
-          while (!mbar_try_wait(&s.full[i % S::STAGES], i / S::STAGES & 1) && globaltimer() - t0 < WAIT_LIMIT_NS) {
-          }
+          wait_at_end(&s.full[i % S::STAGES], i / S::STAGES & 1, dead);
         }
       }
     }
@@ -615,7 +615,7 @@ __global__ void __launch_bounds__(ST_THREADS, StreamShape<BT>::CTAS)
     constexpr uint32_t idesc = umma_idesc(ST_N, BT);
     const uint64_t db0 = umma_desc(smem_addr(s.b[0])), da0 = umma_desc(smem_addr(s.a[0]));
     unsigned it = 0;
-    for (int t = first; t < items && !*dead; t += step) {
+    for (int t = first; t < items && !dead; t += step) {
       for (int c = c0; c < c1; ++c, ++it) {
         const int st = it % S::STAGES, ac = it % S::ACC;
         const bool ok = wait_both_or_die(&s.acc_empty[ac], (it / S::ACC & 1) ^ 1, &s.full[st], it / S::STAGES & 1, dead);
@@ -632,9 +632,7 @@ __global__ void __launch_bounds__(ST_THREADS, StreamShape<BT>::CTAS)
       }
     }
     if (elect_one()) umma_commit(&s.drain);
-    const unsigned long long t0 = globaltimer();
-    while (!mbar_try_wait(&s.drain, 0) && globaltimer() - t0 < WAIT_LIMIT_NS) {
-    }
+    wait_at_end(&s.drain, 0, dead);
   } else {
     // thread r of these 128: column n0 + r of the tile, all BT rows
     const int quarter = warp & 3, r = quarter * 32 + lane;
@@ -691,7 +689,7 @@ __global__ void __launch_bounds__(ST_THREADS, StreamShape<BT>::CTAS)
       bar_sync(1, 128);  // the scale buffers are free for the next item
       const int64_t n = n0 + r;
       if (splits == 1) {
-        const bool lost = *dead;
+        const bool lost = (bool)dead;
 #pragma unroll
         for (int j0 = 0; j0 < BT; j0 += 8) {
           if (j0 < rows && n < p.a.n) {
@@ -706,13 +704,15 @@ __global__ void __launch_bounds__(ST_THREADS, StreamShape<BT>::CTAS)
       }
       // every CTA of the cluster adds a share of the rows, over the CTAs in order
       if (round > 0) wait_cluster_or_die(&s.red_free, (round - 1) & 1, dead);
+      // a CTA that gave up has no sum to give: NaN, which every CTA's share of the rows takes over
+      const bool none = (bool)dead;
 #pragma unroll
-      for (int j = 0; j < BT; ++j) s.red[j][r] = acc[j];
+      for (int j = 0; j < BT; ++j) s.red[j][r] = none ? NAN : acc[j];
       __syncwarp();
       if (lane < splits) peer_arrive(peer_addr(smem_addr(&s.red_full), lane));
       wait_cluster_or_die(&s.red_full, round & 1, dead);
       __syncwarp();
-      const bool lost = *dead;
+      const bool lost = (bool)dead;
       const int j0 = rows * rank / splits, j1 = rows * (rank + 1) / splits;
       // eight rows at a time of all CTAs: no load waits for another, nor for a branch (rows past the share are read and
       // dropped; loads behind a condition each took 5500 cycles for six rows of three CTAs)

@@ -8,6 +8,7 @@
 #include <cstring>
 #include <mutex>
 
+#include "../../../include/ts_moe_debug.h"
 #include "../../../include/ts_moe_ops.h"
 #include "../errors.h"
 #include "act.cuh"
@@ -277,7 +278,7 @@ ts_moe_status ts_moe_act_quant(const ts_moe_act_quant_args* args, void* stream) 
   return done(launch(k, dim3(grid), ACT_THREADS, 0, stream, a, quads, warps / quads, warps % quads), "act_quant launch");
 }
 
-ts_moe_status ts_moe_fp8_matmul(const ts_moe_fp8_matmul_args* args, void* stream) {
+static ts_moe_status fp8_matmul(const ts_moe_fp8_matmul_args* args, int held, unsigned held_us, void* stream) {
   if (!args) return bad("fp8_matmul: args is NULL");
   const ts_moe_fp8_matmul_args& a = *args;
   if (a.rows < 0 || a.rows > TS_MOE_MAX_ROWS) return bad("fp8_matmul: rows must be in [0, 2^24]");
@@ -304,11 +305,14 @@ ts_moe_status ts_moe_fp8_matmul(const ts_moe_fp8_matmul_args* args, void* stream
   p.a = a;
   p.kb = cdiv(a.k, SCALE_BLOCK);
   p.splits = plan.splits;
+  p.held = held;
+  p.held_us = held_us;
   // strides no row or matrix follows may be anything: give the map valid ones
   const int64_t row = (a.k + 15) / 16 * 16, ld_a = a.rows > 1 ? a.ld_a : row, ld_b = a.n > 1 ? a.ld_b : row;
   const int64_t group = a.num_groups > 1 ? a.b_group : (int64_t)a.n * ld_b;
   cudaError_t e;
   if (plan.kind == MatmulPlan::ROWS) {
+    if (held >= 0) return bad("fp8_matmul: this call has no waits");
     p.out_map = 0;
     auto k = a.rows <= 8 ? fp8_row_kernel<1> : fp8_row_kernel<2>;
     e = launch(k, dim3(plan.grid), RW_THREADS, 0, stream, p);
@@ -327,6 +331,14 @@ ts_moe_status ts_moe_fp8_matmul(const ts_moe_fp8_matmul_args* args, void* stream
   else
     e = plan.bt == 16 ? launch_stream<16>(p, ma, mb, plan.grid, stream) : launch_stream<32>(p, ma, mb, plan.grid, stream);
   return done(e, "fp8_matmul launch");
+}
+
+ts_moe_status ts_moe_fp8_matmul(const ts_moe_fp8_matmul_args* args, void* stream) { return fp8_matmul(args, -1, 0, stream); }
+
+ts_moe_status ts_moe_debug_fp8_matmul_held(const ts_moe_fp8_matmul_args* args, int cta, uint32_t wait_us, void* stream) {
+  if (cta < 0) return bad("fp8_matmul: cta must not be negative");
+  if (wait_us > WAIT_LIMIT_US) return bad("fp8_matmul: wait_us is above the limit of the kernels' waits");
+  return fp8_matmul(args, cta, wait_us, stream);
 }
 
 static int balance_ctas(int rows, int experts) {

@@ -8,8 +8,8 @@
 namespace tsm {
 
 // ----------------------------------------------------------------------------- waits
-// Waits for the phase with `parity` of `bar`; gives up after WAIT_LIMIT_NS, or when another thread of the CTA has,
-// and marks the CTA dead.  The clock and the mark are looked at once in WAIT_TRIES tries: both reads take longer than
+// Waits for the phase with `parity` of `bar`; gives up after dead.limit() nanoseconds, or when another thread of the CTA
+// has, and marks the CTA dead.  The clock and the mark are looked at once in WAIT_TRIES tries: both reads take longer than
 // a try, and a wait that ends meanwhile would be noticed late.  wait_cluster_or_die sees
 // what the cluster's other CTAs wrote before their arrivals.
 constexpr unsigned WAIT_TRIES = 64;
@@ -36,30 +36,50 @@ TSM_DEV bool mbar_test(uint64_t* bar, unsigned parity) {
   return ok != 0;
 }
 
+constexpr unsigned WAIT_LIMIT_US = WAIT_LIMIT_NS / 1000;
+
+// The CTA's mark, and how long its waits last: WAIT_LIMIT_NS, but for a CTA that a test holds back.
+struct DeadMark {
+  int set;
+  unsigned limit_us;
+};
+struct Dead {
+  volatile DeadMark* mark;
+  TSM_DEV explicit operator bool() const { return mark->set != 0; }
+  TSM_DEV void set() const { mark->set = 1; }
+  TSM_DEV unsigned long long limit() const { return mark->limit_us * 1000ull; }
+};
+
 // `ready` tries once.
 template <typename Try>
-TSM_DEV bool bounded_wait(const Try& ready, volatile int* dead) {
+TSM_DEV bool bounded_wait(const Try& ready, const Dead& dead) {
   unsigned long long t0 = 0;
   while (true) {
     for (unsigned i = 0; i < WAIT_TRIES; ++i)
       if (ready()) return true;
-    if (*dead) return false;
+    if (dead) return false;
     const unsigned long long now = globaltimer();
     if (t0 == 0) t0 = now;
-    if (now - t0 > WAIT_LIMIT_NS) {
-      *dead = 1;
+    if (now - t0 > dead.limit()) {
+      dead.set();
       return false;
     }
   }
 }
-TSM_DEV bool wait_or_die(uint64_t* bar, unsigned parity, volatile int* dead) {
+TSM_DEV bool wait_or_die(uint64_t* bar, unsigned parity, const Dead& dead) {
   return bounded_wait([&] { return mbar_try_wait(bar, parity); }, dead);
 }
-TSM_DEV bool wait_cluster_or_die(uint64_t* bar, unsigned parity, volatile int* dead) {
+TSM_DEV bool wait_cluster_or_die(uint64_t* bar, unsigned parity, const Dead& dead) {
   return bounded_wait([&] { return try_wait_cluster(bar, parity); }, dead);
 }
+// The same where the mark says nothing (the CTA's copies and MMAs in flight, at its end).
+TSM_DEV void wait_at_end(uint64_t* bar, unsigned parity, const Dead& dead) {
+  const unsigned long long t0 = globaltimer(), limit = dead.limit();
+  while (!mbar_try_wait(bar, parity) && globaltimer() - t0 < limit) {
+  }
+}
 // Two barriers at once: the tries run side by side.
-TSM_DEV bool wait_both_or_die(uint64_t* a, unsigned pa, uint64_t* b, unsigned pb, volatile int* dead) {
+TSM_DEV bool wait_both_or_die(uint64_t* a, unsigned pa, uint64_t* b, unsigned pb, const Dead& dead) {
   return bounded_wait(
       [&] {
         const bool x = mbar_try_wait(a, pa), y = mbar_try_wait(b, pb);

@@ -1,4 +1,6 @@
 """The operators next to the routed half on the GPU where exactness, extreme values or a failure path is the point."""
+import ctypes as C
+
 import pytest
 import torch
 
@@ -55,3 +57,74 @@ def test_act_codes_are_the_quotients(B, M, inter, dtype):
     q, s = R.rows8(M, inter), torch.empty(M, R.blocks(inter), device="cuda")
     B.act_quant(gate, up, 0, q, s)
     same_codes(q, s, 64.0 * up.float())
+
+
+# ----------------------------------------------------------------------------- a wait that runs out
+
+def held_product(B, cta, a, sa, b, sb, out, offsets=None, wait_us=1000):
+    """fp8_matmul in which one CTA issues no copies and gives its waits up after a millisecond; contiguous tensors."""
+    M, K, N = a.shape[0], a.shape[1], out.shape[1]
+    G = 1 if offsets is None else b.shape[0]
+    args = B.Fp8MatmulArgs(rows=M, n=N, k=K, num_groups=G, out_type={BF16: 0, FP16: 1, FP32: 2}[out.dtype], reserved=0,
+                           a=a.data_ptr(), ld_a=a.stride(0), a_scale=sa.data_ptr(), as_row=sa.stride(0), as_block=sa.stride(1),
+                           b=b.data_ptr(), ld_b=b.stride(-2), b_group=b.stride(0) if G > 1 else 0, b_scale=sb.data_ptr(),
+                           bs_group=sb.stride(0) if G > 1 else 0, bs_row=sb.stride(-2), bs_block=sb.stride(-1),
+                           offsets=None if offsets is None else offsets.data_ptr(), add=None, ld_add=0,
+                           out=out.data_ptr(), ld_out=out.stride(0))
+    st = B.lib.ts_moe_debug_fp8_matmul_held(C.byref(args), cta, wait_us, torch.cuda.current_stream().cuda_stream)
+    assert st == 0, B.lib.ts_moe_last_error(None)
+
+
+def lost_tiles(out, want, starts, rows, cols):
+    """Of the tiles (rows from each of `starts`, `cols` columns), the ones that are NaN; the others have to equal `want`."""
+    lost = []
+    for r0, r1 in starts:
+        for m in range(r0, r1, rows):
+            for n in range(0, out.shape[1], cols):
+                t, w = out[m:min(m + rows, r1), n:n + cols], want[m:min(m + rows, r1), n:n + cols]
+                if t.isnan().all():
+                    lost.append((m, n))
+                else:
+                    assert torch.equal(t, w), (m, n)
+    return lost
+
+
+# K split over 2 and 3 CTAs of a cluster; tiles of 128 x 256 that a CTA takes one after another
+@pytest.mark.parametrize("M,N,K,rows,cols", [(64, 4096, 4096, 32, 128), (16, 5760, 2880, 16, 128), (2000, 5000, 300, 128, 256)])
+@pytest.mark.parametrize("cta", [0, 1, 5])
+def test_fp8_matmul_wait_that_runs_out_gives_nan(B, M, N, K, rows, cols, cta):
+    """A CTA whose copies never come: the outputs that need its sums are NaN, all others are as ever, and so is the next call."""
+    r = gen(M)
+    a, sa = R.encode_rows(r(M, K))
+    b, sb = R.encode_matrix(r(N, K))
+    want, out = torch.empty(M, N, device="cuda"), torch.full((M, N), 3.0, device="cuda")
+    B.fp8_matmul(a, sa, b, sb, want)
+    held_product(B, cta, a, sa, b, sb, out)
+    torch.cuda.synchronize()
+    tiles = -(-M // rows) * -(-N // cols)
+    lost = lost_tiles(out, want, [(0, M)], rows, cols)
+    assert 1 <= len(lost) <= -(-tiles // 148), lost
+    B.fp8_matmul(a, sa, b, sb, out)
+    assert torch.equal(out, want)
+
+
+def test_fp8_matmul_wait_that_runs_out_in_a_group(B):
+    """The same where a CTA takes whole items of small groups, K unsplit."""
+    G, each, N, K = 32, 2, 1024, 512
+    r = gen(2)
+    a, sa = R.encode_rows(r(G * each, K))
+    b = torch.empty(G, N, K, dtype=torch.uint8, device="cuda").view(torch.float8_e4m3fn)
+    sb = torch.empty(G, R.blocks(N), R.blocks(K), device="cuda")
+    for g in range(G):
+        q, s = R.encode_matrix(r(N, K))
+        b[g].copy_(q)
+        sb[g].copy_(s)
+    offsets = torch.arange(0, G * each + 1, each, dtype=torch.int32, device="cuda")
+    want, out = torch.empty(G * each, N, device="cuda"), torch.full((G * each, N), 3.0, device="cuda")
+    B.fp8_matmul(a, sa, b, sb, want, offsets=offsets)
+    held_product(B, 7, a, sa, b, sb, out, offsets)
+    torch.cuda.synchronize()
+    lost = lost_tiles(out, want, [(g * each, g * each + each) for g in range(G)], 16, 128)
+    assert len(lost) == 1, lost
+    B.fp8_matmul(a, sa, b, sb, out, offsets=offsets)
+    assert torch.equal(out, want)
