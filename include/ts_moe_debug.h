@@ -1,6 +1,6 @@
 /*
  * ts_moe_debug.h -- helpers exported for tests.  All but the last two expose the
- * pure arithmetic the kernels use to split work between CTAs and the open-time
+ * pure arithmetic that splits work between CTAs and the open-time
  * validation, so both can be checked on a machine without a GPU; they touch
  * neither device memory nor the CUDA runtime.  The last two let a test make a
  * bounded wait run out: one changes a handle's device counters, one runs a
@@ -41,6 +41,13 @@ int ts_moe_debug_coresident(int per_sm, int sm_count, int nb);
 /* The validation ts_moe_open performs before any CUDA call; same status and
  * message (ts_moe_last_error(NULL)). */
 ts_moe_status ts_moe_debug_validate(const ts_moe_config* cfg, const ts_moe_layer_weights* layers);
+
+/* How ts_moe_fp8_matmul would run `args` on `sms` SMs (sizes, output layout and
+ * whether offsets and add are given count; nothing is read through the
+ * pointers): plan[0] the kernel (0 rows, 1 stream, 2 tile), plan[1] rows of a
+ * streaming tile, plan[2] CTAs that share K, plan[3] clusters (CTAs where K is
+ * whole) launched. */
+void ts_moe_debug_fp8_matmul_plan(const ts_moe_fp8_matmul_args* args, int sms, int32_t plan[4]);
 
 /* Failure-path test hook.  Synchronises `stream`, then marks the handle so
  * that in the next layer-kernel launch CTA 0 does not arrive at the grid

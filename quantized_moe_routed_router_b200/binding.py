@@ -116,6 +116,8 @@ def _load():
     lib.ts_moe_rmsnorm.argtypes = [C.POINTER(RmsnormArgs), vp]
     lib.ts_moe_act_quant.argtypes = [C.POINTER(ActQuantArgs), vp]
     lib.ts_moe_fp8_matmul.argtypes = [C.POINTER(Fp8MatmulArgs), vp]
+    lib.ts_moe_debug_fp8_matmul_plan.argtypes = [C.POINTER(Fp8MatmulArgs), i32, C.POINTER(C.c_int32)]
+    lib.ts_moe_debug_fp8_matmul_plan.restype = None
     lib.ts_moe_debug_fp8_matmul_held.argtypes = [C.POINTER(Fp8MatmulArgs), i32, C.c_uint32, vp]
     lib.ts_moe_balance.argtypes = [C.POINTER(BalanceArgs), vp]
     lib.ts_moe_balance_workspace.argtypes = [C.c_int32, C.c_int32]

@@ -540,7 +540,7 @@ struct StreamSmem {
   uint8_t a[S::STAGES][BT * SCALE_BLOCK];
   float red[BT][ST_N];              // this CTA's share of K, for the cluster's CTAs to add
   float scale[2][ST_CHUNK][BT];     // sa * sb of the blocks at hand
-  uint64_t full[S::STAGES], empty[S::STAGES], acc_full[S::ACC], acc_empty[S::ACC], red_full, red_free, drain;
+  uint64_t full[S::STAGES], empty[S::STAGES], acc_full[S::ACC], acc_empty[S::ACC], red_full, drain;
   uint32_t tmem;
   DeadMark dead;
   GroupTable groups;
@@ -562,7 +562,6 @@ __global__ void __launch_bounds__(ST_THREADS, StreamShape<BT>::CTAS)
     for (int i = 0; i < S::STAGES; ++i) mbar_init(&s.full[i], 1), mbar_init(&s.empty[i], 1);
     for (int i = 0; i < S::ACC; ++i) mbar_init(&s.acc_full[i], 1), mbar_init(&s.acc_empty[i], 4);
     mbar_init(&s.red_full, 4 * splits);
-    mbar_init(&s.red_free, 4 * splits);
     mbar_init(&s.drain, 1);
     s.dead.set = 0;
     s.dead.limit_us = (int)blockIdx.x == p.held ? p.held_us : WAIT_LIMIT_US;
@@ -639,8 +638,8 @@ __global__ void __launch_bounds__(ST_THREADS, StreamShape<BT>::CTAS)
     const uint32_t mine = tmem + ((uint32_t)(quarter * 32) << 16);
     constexpr int PER = ST_CHUNK * BT / 128;  // scales a thread stages per chunk
     const int type = p.a.out_type;
-    unsigned it = 0, round = 0;
-    for (int t = first; t < items; t += step, ++round) {
+    unsigned it = 0;
+    for (int t = first; t < items; t += step) {
       const int tt = t == first ? t0 : t / nt, g = group_of(s.groups, p.a.num_groups, tt);
       const int m0 = s.groups.lo[g] + (tt - s.groups.first[g]) * BT, rows = min(BT, s.groups.lo[g + 1] - m0);
       const int n0 = t == first ? n00 : (t - tt * nt) * ST_N;
@@ -702,15 +701,15 @@ __global__ void __launch_bounds__(ST_THREADS, StreamShape<BT>::CTAS)
         }
         continue;
       }
-      // every CTA of the cluster adds a share of the rows, over the CTAs in order
-      if (round > 0) wait_cluster_or_die(&s.red_free, (round - 1) & 1, dead);
-      // a CTA that gave up has no sum to give: NaN, which every CTA's share of the rows takes over
+      // Every CTA of the cluster adds a share of the rows, over the CTAs in order.  K is split only where the grid has a
+      // cluster for every item (matmul_plan), so this is the cluster's one item and s.red is written once.  A CTA that gave up
+      // has no sum to give: NaN, which every CTA's share of the rows takes over.
       const bool none = (bool)dead;
 #pragma unroll
       for (int j = 0; j < BT; ++j) s.red[j][r] = none ? NAN : acc[j];
       __syncwarp();
       if (lane < splits) peer_arrive(peer_addr(smem_addr(&s.red_full), lane));
-      wait_cluster_or_die(&s.red_full, round & 1, dead);
+      wait_cluster_or_die(&s.red_full, 0, dead);
       __syncwarp();
       const bool lost = (bool)dead;
       const int j0 = rows * rank / splits, j1 = rows * (rank + 1) / splits;
@@ -733,7 +732,7 @@ __global__ void __launch_bounds__(ST_THREADS, StreamShape<BT>::CTAS)
             for (int j = 0; j < R; ++j) w[q][j] = 0.f;
           }
         }
-if (n < p.a.n) {
+        if (n < p.a.n) {
           if (p.a.add) load_column<R>(p.a.add, type, p.a.ld_add, m0 + jb, min(j1 - jb, R), n, d);
 #pragma unroll
           for (int j = 0; j < R; ++j) {
@@ -745,8 +744,7 @@ if (n < p.a.n) {
           store_column<R>(p.a.out, type, p.a.ld_out, m0 + jb, min(j1 - jb, R), n, d);
         }
       }
-      __syncwarp();
-      if (lane < splits) peer_arrive(peer_addr(smem_addr(&s.red_free), lane));
+      break;
     }
   }
   __syncwarp();

@@ -172,9 +172,10 @@ MatmulPlan matmul_plan(const ts_moe_fp8_matmul_args& a, int sms) {
   const int bt = mean <= 16 ? 16 : 32;
   const int64_t items = (cdiv(a.rows, bt) + reached - 1) * cdiv(a.n, ST_N);
   // K is split while that leaves one CTA an SM, or two where one would leave K whole, never into a second wave: a cluster
-  // joins its shares in about a microsecond, at every item (64 x 4096 x 4096, with an earlier, slower join: whole 14.8,
+  // joins its shares in about a microsecond (64 x 4096 x 4096, with an earlier, slower join: whole 14.8,
   // 2 ways 11.5, 4 ways 11.4, 8 ways 25.0).
   const int splits = (int)std::max<int64_t>(1, std::min<int64_t>(std::min(MAX_SPLITS, kb), (items * 2 <= sms ? sms : 2 * sms) / items));
+  // A split makes at most sms or 2 sms CTAs of all items: every cluster has one item, as the kernel's join needs it.
   const MatmulPlan stream = {MatmulPlan::STREAM, bt, splits, (int)std::min<int64_t>(items, 2 * sms / splits)};
   if (G > 1) return stream;
   // One matrix: what each would take, by 0.5 a block of K and tile against a fixed 5 and the larger of 0.13 a block in
@@ -334,6 +335,14 @@ static ts_moe_status fp8_matmul(const ts_moe_fp8_matmul_args* args, int held, un
 }
 
 ts_moe_status ts_moe_fp8_matmul(const ts_moe_fp8_matmul_args* args, void* stream) { return fp8_matmul(args, -1, 0, stream); }
+
+void ts_moe_debug_fp8_matmul_plan(const ts_moe_fp8_matmul_args* args, int sms, int32_t plan[4]) {
+  const MatmulPlan p = matmul_plan(*args, sms);
+  plan[0] = p.kind;
+  plan[1] = p.bt;
+  plan[2] = p.splits;
+  plan[3] = p.grid;
+}
 
 ts_moe_status ts_moe_debug_fp8_matmul_held(const ts_moe_fp8_matmul_args* args, int cta, uint32_t wait_us, void* stream) {
   if (cta < 0) return bad("fp8_matmul: cta must not be negative");

@@ -1,11 +1,44 @@
-"""Further refusals of the operators next to the routed half, on a machine without a GPU."""
+"""Further host logic and refusals of the operators next to the routed half, on a machine without a GPU."""
+import ctypes as C
+import math
+import random
+
 import pytest
 
 from tests.test_ops_host import B, matmul_args  # noqa: F401  (B is a fixture)
-import ctypes as C
 
 
 @pytest.mark.parametrize("cta,wait_us,frag", [(-1, 1, "cta"), (0, 2_000_001, "wait_us")])
 def test_held_product_refusals(B, cta, wait_us, frag):  # noqa: F811
     st = B.lib.ts_moe_debug_fp8_matmul_held(C.byref(matmul_args(B)), cta, wait_us, None)
     assert st == 1 and frag in B.lib.ts_moe_last_error(None).decode()
+
+
+def test_a_split_product_has_a_cluster_for_every_item(B):  # noqa: F811
+    """The cluster's join takes one item: wherever K is split, the grid has as many clusters as there can be items (row
+    tiles of all groups at their most, times column tiles), and its CTAs fit two an SM."""
+    rng = random.Random(7)
+    seen = set()
+    for _ in range(20000):
+        size = lambda low, high: int(math.exp(rng.uniform(math.log(low), math.log(high + 1))))  # noqa: E731
+        G = rng.choice((0, 0, 1, 2, 8, 32, 100, 256))
+        M, N, K, sms = size(1, 8192), size(1, 20000), size(1, 20000), rng.choice((148, 148, 132, 16))
+        a = matmul_args(B, rows=M, n=N, k=K, num_groups=max(G, 1), ld_out=N, out_type=rng.choice((0, 2)))
+        if not G:
+            a.offsets = None
+        if rng.random() < 0.7:
+            a.add = None
+        plan = (C.c_int32 * 4)()
+        B.lib.ts_moe_debug_fp8_matmul_plan(C.byref(a), sms, plan)
+        kind, bt, splits, grid = plan
+        seen.add((kind, splits))
+        assert splits >= 1 and grid >= 1
+        if kind != 1:
+            assert splits == 1
+            continue
+        # groups of sizes that leave the most row tiles: one row each, and the rest in one
+        reached = min(max(G, 1), M)
+        items = (reached - 1 + -(-(M - reached + 1) // bt)) * -(-N // 128)
+        assert splits <= min(4, -(-K // 128)) and grid * splits <= 2 * sms
+        assert splits == 1 or grid >= items, (M, N, K, G, sms, list(plan))
+    assert {(0, 1), (1, 1), (1, 2), (1, 4), (2, 1)} <= seen
