@@ -3,6 +3,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <cfloat>
 #include <cmath>
 #include <cstdio>
 #include <cstring>
@@ -215,6 +216,26 @@ cudaError_t launch_norm(const ts_moe_rmsnorm_args& a, bool vec, void* stream) {
   return launch(k, dim3(a.rows), threads, 0, stream, a);
 }
 
+// The largest bits of a gate in memory whose sigmoid is not a far one: those of -64, or of -64 / alpha rounded towards 0.
+// Above them are larger negative gates and negative NaN.  With a negative alpha any gate may be far.
+uint32_t act_far_bits(const ts_moe_act_quant_args& a) {
+  const float alpha = a.act == TS_ACT_SWIGLU ? 1.f : a.act_alpha;
+  if (alpha < 0.f) return 0;
+  const float t = std::min(-FAR / alpha, FLT_MAX);  // alpha = 0: no finite gate is far
+  uint32_t bits;
+  std::memcpy(&bits, &t, sizeof(bits));
+  if (a.in_type == TS_DT_FP32) return bits | 0x80000000u;
+  if (a.in_type == TS_DT_BF16) return bits >> 16 | 0x8000u;
+  if (t >= 65504.f) return 0xFBFFu;          // fp16's largest
+  if (t < 0x1p-14f) return 0x8000u;          // below its normal range: every negative gate
+  return 0x8000u | ((bits >> 13) - (112u << 10));
+}
+
+template <bool CLAMPED>
+auto act_instance(bool vec, bool wide) {
+  return vec ? (wide ? act_quant_kernel<true, true, CLAMPED> : act_quant_kernel<true, false, CLAMPED>) : act_quant_kernel<false, false, CLAMPED>;
+}
+
 template <bool SIGMOID, bool WIDE>
 void (*balance_instance(int experts))(const BalanceParams) {
   const int lanes = balance_lanes(experts);
@@ -275,8 +296,8 @@ ts_moe_status ts_moe_act_quant(const ts_moe_act_quant_args* args, void* stream) 
   const int resident = vec && wide ? 2 : 4;  // CTAs per SM by the kernel's launch bounds
   const int grid = (int)std::min<int64_t>((units + ACT_THREADS / 32 - 1) / (ACT_THREADS / 32), 148 * resident);
   const int warps = grid * (ACT_THREADS / 32);
-  auto k = vec ? (wide ? act_quant_kernel<true, true> : act_quant_kernel<true, false>) : act_quant_kernel<false, false>;
-  return done(launch(k, dim3(grid), ACT_THREADS, 0, stream, a, quads, warps / quads, warps % quads), "act_quant launch");
+  auto k = a.act == TS_ACT_SWIGLU ? act_instance<false>(vec, wide) : act_instance<true>(vec, wide);
+  return done(launch(k, dim3(grid), ACT_THREADS, 0, stream, a, quads, warps / quads, warps % quads, act_far_bits(a)), "act_quant launch");
 }
 
 static ts_moe_status fp8_matmul(const ts_moe_fp8_matmul_args* args, int held, unsigned held_us, void* stream) {

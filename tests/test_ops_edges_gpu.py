@@ -128,3 +128,41 @@ def test_fp8_matmul_wait_that_runs_out_in_a_group(B):
     assert len(lost) == 1, lost
     B.fp8_matmul(a, sa, b, sb, out, offsets=offsets)
     assert torch.equal(out, want)
+
+
+# ----------------------------------------------------------------------------- far below the sigmoid's own range
+
+# e^x from an exponent rounded once, which turns into |x| half steps (|x| <= 180 here), two exponentials of 2 ulp and four
+# products; the clamped form's alpha g adds its own rounding, another |x| half steps
+FAR_REL = (2 * 180 + 2 * 4 + 8) * R.F32
+
+
+@pytest.mark.parametrize("inter", [256, 250])
+@pytest.mark.parametrize("dtype", [BF16, FP32])
+@pytest.mark.parametrize("kind,alpha,limit", [(0, 1.0, 7.0), (1, 1.0, 1e38), (1, 2.0, 1e36)])
+def test_act_quant_of_gates_far_below_zero(B, inter, dtype, kind, alpha, limit):
+    """silu(g) up with g from -60 to -180 and up large enough for values that a scale reaches: e^g alone is below the
+    smallest float32 from -104 on, the product is not.  One far gate among ordinary ones in the last rows."""
+    M = 24
+    r = gen(inter)
+    g = -torch.linspace(60, 170, M, device="cuda")[:, None] / alpha * (1 + 0.05 * torch.rand(M, inter, device="cuda"))
+    u = torch.where(r(M, inter) > 0, 1.0, -1.0) * torch.exp2(120 + 2 * torch.rand(M, inter, device="cuda"))
+    u[:4] *= 2.0 ** -100
+    g[20:, :128], u[20:, :128] = r(4, 128), r(4, 128)
+    g[20:, 5] = -90.0 / alpha
+    u[20:, 5] = 1e30
+    g, u = g.to(dtype), u.to(dtype)
+    q, s = R.rows8(M, inter), torch.empty(M, R.blocks(inter), device="cuda")
+    B.act_quant(g, u, kind, q, s, act_alpha=alpha, act_limit=limit)
+    v = R.act(g, u, kind, alpha, limit)
+    R.check_rows8(q, s, v, FAR_REL)
+    assert (q[:12].float() != 0).any(1).all()
+
+
+def test_act_quant_of_infinite_gates(B):
+    """silu(-inf) is no number, as its formula has it, in the group that holds it and nowhere else."""
+    g, u = gen(1)(3, 256), gen(2)(3, 256)
+    g[1, 200] = -float("inf")
+    q, s = R.rows8(3, 256), torch.empty(3, 2, device="cuda")
+    B.act_quant(g, u, 0, q, s)
+    assert s[1, 1].isnan() and s.isnan().sum() == 1
