@@ -252,16 +252,19 @@ __global__ void __launch_bounds__(BAL_THREADS) balance_kernel(const BalanceParam
         slope[i] = u * t[i];
       }
       reduce();
-      if (__any_sync(0xFFFFFFFFu, s < 0.25f)) {
-        // a row of very negative logits, whose sigmoids would lose their smallest: all of them times e^-m, m = min(max l, 0)
+      const bool small = s < 0.25f;  // the same in all lanes of the row
+      if (__any_sync(0xFFFFFFFFu, small)) {
+        // a row of very negative logits, whose sigmoids would lose their smallest: all of them times e^-m, m = min(max l, 0).
+        // The warp's other rows keep what they have: a row's bits do not depend on the rows beside it.
         float l[N];
         logits_of(now, l);
         const float top = row_max(l), m = top == -INFINITY ? 0.f : fminf(top, 0.f);
 #pragma unroll
         for (int i = 0; i < N; ++i) {
           const float u = ex2(min_nan(-LOG2E * l[i], 127.f));
-          slope[i] = l[i] < -60.f ? 1.f : u * rcp(1.f + u);  // from e^87 on the reciprocal is below the normal range
-          if (m < 0.f) t[i] = ex2(LOG2E * (l[i] - m)) * slope[i];
+          const float far = l[i] < -60.f ? 1.f : u * rcp(1.f + u);  // from e^87 on the reciprocal is below the normal range
+          if (small) slope[i] = far;
+          if (small && m < 0.f) t[i] = ex2(LOG2E * (l[i] - m)) * far;
         }
         reduce();
       }

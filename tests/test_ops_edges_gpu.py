@@ -166,3 +166,24 @@ def test_act_quant_of_infinite_gates(B):
     q, s = R.rows8(3, 256), torch.empty(3, 2, device="cuda")
     B.act_quant(g, u, 0, q, s)
     assert s[1, 1].isnan() and s.isnan().sum() == 1
+
+
+# ----------------------------------------------------------------------------- rows of a router's batch
+
+@pytest.mark.parametrize("E", [8, 60, 256])
+def test_balance_gradient_of_a_row_does_not_depend_on_its_neighbours(B, E):
+    """With one idx (so one load), other rows' logits change nothing in a row's gradient, not even its last bits: rows of
+    negative logits beside ones whose sigmoids all but vanish."""
+    M = 640
+    l = gen(E)(M, E) - 3.0
+    idx = l.topk(4, -1).indices.to(torch.int32)
+
+    def gradient(logits):
+        loss, counts, d = torch.empty(1, device="cuda"), torch.empty(E, dtype=torch.int32, device="cuda"), torch.empty_like(logits)
+        B.balance(logits, idx, 2, loss, counts, dlogits=d)
+        return d
+
+    beside = l.clone()
+    beside[1::3] -= 40.0
+    want, got = gradient(l), gradient(beside)
+    assert torch.equal(got[0::3], want[0::3]) and torch.equal(got[2::3], want[2::3])
