@@ -5,7 +5,7 @@ import pytest
 import torch
 
 from tests import ops_ref as R
-from tests.test_ops_gpu import BF16, FP16, FP32, gen
+from tests.test_ops_gpu import BF16, FP16, FP32, gen, routed, run_balance
 
 pytestmark = pytest.mark.gpu
 
@@ -187,3 +187,61 @@ def test_balance_gradient_of_a_row_does_not_depend_on_its_neighbours(B, E):
     beside[1::3] -= 40.0
     want, got = gradient(l), gradient(beside)
     assert torch.equal(got[0::3], want[0::3]) and torch.equal(got[2::3], want[2::3])
+
+
+def gradient_bound(logits, idx, score, mask, coef, dloss):
+    """(gradient in 64 bits, what float32 may leave it off by), element by element and in proportion to p (1 - sigmoid):
+
+    p = t / sum t.  t: an exponential (2 ulp = 4 half steps) whose argument d (l - max, or l) is rounded as a difference, by
+    the constant and as a product, 3 |d| half steps; for sigmoids also a sum and a reciprocal, 1 + 4.  The sum: at most
+    8 + 5 additions of positive terms.  The quotient: a reciprocal and a product, 4 + 1.  1 - sigmoid: as t, and a product.
+    f: 3 roundings.  sum f p: as p, f, and 13 additions.  The rest: 3 of coef dloss / T, and 4 products and a difference."""
+    l = R.d64(logits)
+    M, E = l.shape
+    *_, counts, grad = R.balance(logits, idx, score, mask, coef, dloss)
+    T = max(1, M if mask is None else int(mask.sum()))
+    f = counts.double() * E / (idx.shape[1] * T)
+    t = torch.nn.functional.logsigmoid(l) if score == 2 else l
+    p = torch.softmax(t, 1)
+    slope = torch.sigmoid(-l) if score == 2 else torch.ones_like(l)
+    d = float((l - l.max(1, keepdim=True).values).abs().max()) if score != 2 else float(l.abs().max())
+    trel = (3 * d + 4 + (5 if score == 2 else 0)) * R.F32
+    prel = 2 * trel + (13 + 5) * R.F32
+    srel = trel + R.F32 if score == 2 else 0.0
+    fp = (p * f).sum(1, keepdim=True)
+    c = abs(coef * dloss) / T
+    bound = c * p * slope * ((f - fp).abs() * (prel + srel + 8 * R.F32) + 3 * R.F32 * f + fp * (prel + 16 * R.F32))
+    return grad, bound + R.rounding(grad, logits.dtype) + c * f.max() * 2.0 ** -124
+
+
+@pytest.mark.parametrize("score", [0, 1, 2])
+@pytest.mark.parametrize("M,E,K,dtype", [(3, 8, 2, FP32), (65, 40, 4, FP16), (333, 100, 8, FP32), (1000, 256, 8, FP32), (4099, 129, 3, BF16),
+                                         (20000, 64, 6, FP32), (3000, 200, 8, FP16)])
+def test_balance_gradient_element_by_element(B, score, M, E, K, dtype):
+    l, idx = routed(M, E, K, dtype)
+    mask = torch.rand(M, generator=torch.Generator().manual_seed(M)).cuda() > 0.2
+    for m in (None, mask):
+        *_, d = run_balance(B, l, idx, score, m, coef=0.5, dloss=-3.0)
+        want, tol = gradient_bound(l, idx, score, m, 0.5, -3.0)
+        err = (R.d64(d) - want).abs()
+        assert (err <= tol).all(), (err / tol).max()
+
+
+@pytest.mark.parametrize("score", [1, 2])
+@pytest.mark.parametrize("M,E,K", [(400, 256, 8), (1500, 130, 4)])
+def test_balance_gradient_against_differences_over_many_ctas(B, score, M, E, K):
+    """Central differences of the loss in 64 bits, the load held fixed.  Their own error: h^2 / 6 times the third derivative,
+    at most 6 (2 V)^3 times the largest load for shares that move by V (a sigmoid's slope is at most 1; a factor 4 for
+    its own derivatives), and a rounding of the loss over h."""
+    l, idx = routed(M, E, K)
+    *_, d = run_balance(B, l, idx, score, coef=0.5)
+    _, tol = gradient_bound(l, idx, score, None, 0.5, 1.0)
+    f = torch.bincount(idx.flatten().cpu().long(), minlength=E).max().double() * E / (K * M)
+    h, l64 = 1e-6, l.double().cpu()
+    for seed in range(3):
+        u = torch.randn(M, E, generator=torch.Generator().manual_seed(seed), dtype=torch.float64)
+        up, down = (R.balance(l64 + s * h * u, idx, score, coef=0.5)[0] for s in (1, -1))
+        got, want = float((R.d64(d) * u).sum()), (up - down) / (2 * h)
+        room = 0.5 * f * h * h / 6 * 4 * 6 * (2 * u.abs().max()) ** 3 + abs(up) * 2.0 ** -50 / h
+        assert abs(got - want) <= float((tol * u.abs()).sum() + room), (got, want, float(room))
+        assert abs(want) > 20 * float(room)      # the differences say something
