@@ -4,6 +4,7 @@ import math
 import random
 
 import pytest
+import torch
 
 from tests.test_ops_host import B, matmul_args  # noqa: F401  (B is a fixture)
 
@@ -42,3 +43,19 @@ def test_a_split_product_has_a_cluster_for_every_item(B):  # noqa: F811
         assert splits <= min(4, -(-K // 128)) and grid * splits <= 2 * sms
         assert splits == 1 or grid >= items, (M, N, K, G, sms, list(plan))
     assert {(0, 1), (1, 1), (1, 2), (1, 4), (2, 1)} <= seen
+
+
+def test_binding_refuses_tensors_of_other_dimensions(B):  # noqa: F811
+    """As TsMoeError, like every other refusal."""
+    z, q, s = torch.zeros(4, 64), torch.zeros(4, 64, dtype=torch.uint8), torch.zeros(4, 1)
+    line, cube = torch.zeros(64), torch.zeros(2, 4, 64)
+    i32 = torch.int32
+    for call in (lambda: B.rmsnorm(line, None, 1e-5, y=line), lambda: B.rmsnorm(cube, None, 1e-5, y=cube),
+                 lambda: B.rmsnorm(z, None, 1e-5, y=cube), lambda: B.act_quant(line, line, 0, q, s), lambda: B.act_quant(cube, cube, 0, q, s),
+                 lambda: B.fp8_matmul(q[0], s, q, s, z), lambda: B.fp8_matmul(q, s, q, s, line), lambda: B.fp8_matmul(q, s, q[None], s, z),
+                 lambda: B.fp8_matmul(q, s, q[:0][None][:0], torch.zeros(0, 1, 1), z, offsets=torch.zeros(1, dtype=i32)),
+                 lambda: B.balance(line, torch.zeros(64, 2, dtype=i32), 1, torch.zeros(1), torch.zeros(8, dtype=i32)),
+                 lambda: B.balance(z, torch.zeros(4, dtype=i32), 1, torch.zeros(1), torch.zeros(64, dtype=i32)),
+                 lambda: B.balance(z, torch.zeros((), dtype=i32), 1, torch.zeros(1), torch.zeros(64, dtype=i32))):
+        with pytest.raises(B.TsMoeError):
+            call()
