@@ -16,7 +16,8 @@
  *     state between calls; calls on different streams may overlap as long as
  *     their outputs and workspaces differ.
  *   - Strides (ld_*, *_row, ...) count elements; the innermost dimension is
- *     contiguous.  Outputs must not overlap inputs or each other, except where
+ *     contiguous.  Pointers are aligned to their elements, and to more where a
+ *     field says so.  Outputs must not overlap inputs or each other, except where
  *     a field says so.
  *   - 8-bit rows are E4M3 (finite range +-448, 0x7F = NaN) with one float32
  *     scale per 128 consecutive columns of a row, the last group of a row being

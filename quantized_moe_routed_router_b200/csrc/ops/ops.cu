@@ -34,6 +34,10 @@ bool known_type(int t) { return t == TS_DT_BF16 || t == TS_DT_FP16 || t == TS_DT
 bool aligned(const void* p, int64_t ld_bytes, int to) { return (uintptr_t)p % to == 0 && ld_bytes % to == 0; }
 bool aligned_rows(const void* p, int64_t ld, int type) { return !p || aligned(p, ld * dt_size(type), 16); }
 
+// An element's place: loads and stores of elements need it.  NULL passes.
+bool at_elements(const void* p, int type) { return (uintptr_t)p % dt_size(type) == 0; }
+bool at_words(const void* p) { return (uintptr_t)p % 4 == 0; }
+
 // With programmatic dependent launch: the kernel's set-up overlaps the previous kernel's tail, and
 // griddepcontrol.wait orders the data.  cluster: CTAs of a cluster along x.
 template <typename... Params, typename... Args>
@@ -268,6 +272,9 @@ ts_moe_status ts_moe_rmsnorm(const ts_moe_rmsnorm_args* args, void* stream) {
   if (a.ld_resid < a.hidden || (a.delta && a.ld_delta < a.hidden) || (a.resid_out && a.ld_resid_out < a.hidden) ||
       (a.y && a.ld_y < a.hidden) || (a.q && a.ld_q < a.hidden))
     return bad("rmsnorm: a row stride is smaller than hidden");
+  if (!at_elements(a.resid, a.resid_type) || !at_elements(a.delta, a.delta_type) || !at_elements(a.gamma, a.gamma_type) ||
+      !at_elements(a.resid_out, a.resid_type) || !at_elements(a.y, a.y_type) || !at_words(a.q_scale))
+    return bad("rmsnorm: a pointer is not aligned to its elements");
   if (a.resid_out == a.resid && a.ld_resid_out != a.ld_resid && a.resid_out) return bad("rmsnorm: resid_out in place needs resid's stride");
   const bool vec = a.hidden % 8 == 0 && aligned_rows(a.resid, a.ld_resid, a.resid_type) &&
                    aligned_rows(a.delta, a.ld_delta, a.delta_type) && aligned_rows(a.gamma, 0, a.gamma_type) &&
@@ -288,6 +295,8 @@ ts_moe_status ts_moe_act_quant(const ts_moe_act_quant_args* args, void* stream) 
   if (a.rows == 0) return TS_MOE_OK;
   if (!a.gate || !a.up || !a.q || !a.q_scale) return bad("act_quant: gate, up, q and q_scale must be non-NULL");
   if (a.ld_gate < a.inter || a.ld_up < a.inter || a.ld_q < a.inter) return bad("act_quant: a row stride is smaller than inter");
+  if (!at_elements(a.gate, a.in_type) || !at_elements(a.up, a.in_type) || !at_words(a.q_scale))
+    return bad("act_quant: a pointer is not aligned to its elements");
   const bool vec = a.inter % 8 == 0 && aligned_rows(a.gate, a.ld_gate, a.in_type) && aligned_rows(a.up, a.ld_up, a.in_type) &&
                    aligned(a.q, a.ld_q, 8);
   const bool wide = a.in_type == TS_DT_FP32;
@@ -314,6 +323,8 @@ static ts_moe_status fp8_matmul(const ts_moe_fp8_matmul_args* args, int held, un
   if (a.ld_a < a.k || a.ld_b < a.k || a.ld_out < a.n || (a.add && a.ld_add < a.n)) return bad("fp8_matmul: a row stride is smaller than the row");
   if (!aligned(a.a, a.rows > 1 ? a.ld_a : 0, 16) || !aligned(a.b, a.n > 1 ? a.ld_b : 0, 16) || (a.num_groups > 1 && a.b_group % 16))
     return bad("fp8_matmul: the rows of a and b must start at 16-byte boundaries");
+  if (!at_elements(a.out, a.out_type) || !at_elements(a.add, a.out_type) || !at_words(a.a_scale) || !at_words(a.b_scale) || !at_words(a.offsets))
+    return bad("fp8_matmul: a pointer is not aligned to its elements");
   if (a.num_groups > 1 && a.b_group < (int64_t)(a.n - 1) * a.ld_b + a.k) return bad("fp8_matmul: b_group is smaller than a matrix");
   if (a.add == a.out && a.ld_add != a.ld_out) return bad("fp8_matmul: add in place needs out's stride");
   if (a.ld_a >= (int64_t)1 << 40 || a.ld_b >= (int64_t)1 << 40 || a.b_group >= (int64_t)1 << 40)
@@ -397,6 +408,9 @@ ts_moe_status ts_moe_balance(const ts_moe_balance_args* args, void* stream) {
     if (a.ld_logits < a.experts || a.ld_idx < a.top_k || (a.dlogits && a.ld_dlogits < a.experts))
       return bad("balance: a row stride is smaller than the row");
   }
+  if ((a.rows > 0 && (!at_elements(a.logits, a.dtype) || !at_elements(a.dlogits, a.dtype) || !at_words(a.idx))) || !at_words(a.dloss) ||
+      !at_words(a.loss) || !at_words(a.prob) || !at_words(a.counts) || !at_words(a.offsets))
+    return bad("balance: a pointer is not aligned to its elements");
   if (!a.workspace || (uintptr_t)a.workspace % 16) return bad("balance: workspace must be non-NULL and 16-byte aligned");
   if (a.workspace_bytes < ts_moe_balance_workspace(a.rows, a.experts)) return bad("balance: workspace is too small");
 

@@ -6,7 +6,7 @@ import random
 import pytest
 import torch
 
-from tests.test_ops_host import B, matmul_args  # noqa: F401  (B is a fixture)
+from tests.test_ops_host import P, B, act_args, balance_args, matmul_args, norm_args, refused  # noqa: F401  (B is a fixture)
 
 
 @pytest.mark.parametrize("cta,wait_us,frag", [(-1, 1, "cta"), (0, 2_000_001, "wait_us")])
@@ -59,3 +59,18 @@ def test_binding_refuses_tensors_of_other_dimensions(B):  # noqa: F811
                  lambda: B.balance(z, torch.zeros((), dtype=i32), 1, torch.zeros(1), torch.zeros(64, dtype=i32))):
         with pytest.raises(B.TsMoeError):
             call()
+
+
+@pytest.mark.parametrize("op,over", [
+    ("rmsnorm", dict(resid=P + 1, resid_out=P + 1)), ("rmsnorm", dict(resid_type=2, resid=P + 2, resid_out=P + 4)), ("rmsnorm", dict(delta=P + 2)),
+    ("rmsnorm", dict(gamma=P + 6)), ("rmsnorm", dict(y=P + 3)), ("rmsnorm", dict(resid_out=P + 1)), ("rmsnorm", dict(q_scale=P + 2)),
+    ("act_quant", dict(gate=P + 1)), ("act_quant", dict(in_type=2, up=P + 2)), ("act_quant", dict(q_scale=P + 1)),
+    ("fp8_matmul", dict(out=P + 1)), ("fp8_matmul", dict(out_type=2, out=P + 2)), ("fp8_matmul", dict(add=P + 1)),
+    ("fp8_matmul", dict(a_scale=P + 2)), ("fp8_matmul", dict(b_scale=P + 1)), ("fp8_matmul", dict(offsets=P + 2)),
+    ("balance", dict(logits=P + 2)), ("balance", dict(dtype=0, dlogits=P + 1)), ("balance", dict(idx=P + 2)), ("balance", dict(dloss=P + 2)),
+    ("balance", dict(loss=P + 1)), ("balance", dict(prob=P + 2)), ("balance", dict(counts=P + 2)), ("balance", dict(offsets=P + 1)),
+])
+def test_pointers_off_their_elements_are_refused(B, op, over):  # noqa: F811
+    """A load there would fault the GPU."""
+    args = dict(rmsnorm=norm_args, act_quant=act_args, fp8_matmul=matmul_args, balance=balance_args)[op](B, **over)
+    refused(B, getattr(B.lib, "ts_moe_" + op), args, "aligned to its elements")
