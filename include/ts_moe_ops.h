@@ -18,7 +18,8 @@
  *   - Strides (ld_*, *_row, ...) count elements; the innermost dimension is
  *     contiguous.  Pointers are aligned to their elements, and to more where a
  *     field says so.  Outputs must not overlap inputs or each other, except where
- *     a field says so.
+ *     a field says so; scale strides that would put two scales in one place are
+ *     refused.
  *   - 8-bit rows are E4M3 (finite range +-448, 0x7F = NaN) with one float32
  *     scale per 128 consecutive columns of a row, the last group of a row being
  *     short where the width is no multiple of 128; an element is q * scale.

@@ -6,8 +6,10 @@
 #include <cfloat>
 #include <cmath>
 #include <cstdio>
+#include <cstdlib>
 #include <cstring>
 #include <mutex>
+#include <numeric>
 
 #include "../../../include/ts_moe_debug.h"
 #include "../../../include/ts_moe_ops.h"
@@ -37,6 +39,13 @@ bool aligned_rows(const void* p, int64_t ld, int type) { return !p || aligned(p,
 // An element's place: loads and stores of elements need it.  NULL passes.
 bool at_elements(const void* p, int type) { return (uintptr_t)p % dt_size(type) == 0; }
 bool at_words(const void* p) { return (uintptr_t)p % 4 == 0; }
+
+// Whether two of an output's [rows][cols] elements, at row * r + col * c, are one: dr rows and dc columns apart, dr r = dc c.
+bool overlap(int64_t rows, int64_t cols, int64_t r, int64_t c) {
+  const int64_t g = std::gcd(r, c);
+  if (g == 0) return rows > 1 || cols > 1;
+  return std::abs(c / g) < rows && std::abs(r / g) < cols;
+}
 
 // With programmatic dependent launch: the kernel's set-up overlaps the previous kernel's tail, and
 // griddepcontrol.wait orders the data.  cluster: CTAs of a cluster along x.
@@ -275,6 +284,7 @@ ts_moe_status ts_moe_rmsnorm(const ts_moe_rmsnorm_args* args, void* stream) {
   if (!at_elements(a.resid, a.resid_type) || !at_elements(a.delta, a.delta_type) || !at_elements(a.gamma, a.gamma_type) ||
       !at_elements(a.resid_out, a.resid_type) || !at_elements(a.y, a.y_type) || !at_words(a.q_scale))
     return bad("rmsnorm: a pointer is not aligned to its elements");
+  if (a.q && overlap(a.rows, cdiv(a.hidden, SCALE_BLOCK), a.qs_row, a.qs_group)) return bad("rmsnorm: elements of q_scale overlap");
   if (a.resid_out == a.resid && a.ld_resid_out != a.ld_resid && a.resid_out) return bad("rmsnorm: resid_out in place needs resid's stride");
   const bool vec = a.hidden % 8 == 0 && aligned_rows(a.resid, a.ld_resid, a.resid_type) &&
                    aligned_rows(a.delta, a.ld_delta, a.delta_type) && aligned_rows(a.gamma, 0, a.gamma_type) &&
@@ -297,6 +307,7 @@ ts_moe_status ts_moe_act_quant(const ts_moe_act_quant_args* args, void* stream) 
   if (a.ld_gate < a.inter || a.ld_up < a.inter || a.ld_q < a.inter) return bad("act_quant: a row stride is smaller than inter");
   if (!at_elements(a.gate, a.in_type) || !at_elements(a.up, a.in_type) || !at_words(a.q_scale))
     return bad("act_quant: a pointer is not aligned to its elements");
+  if (overlap(a.rows, cdiv(a.inter, SCALE_BLOCK), a.qs_row, a.qs_group)) return bad("act_quant: elements of q_scale overlap");
   const bool vec = a.inter % 8 == 0 && aligned_rows(a.gate, a.ld_gate, a.in_type) && aligned_rows(a.up, a.ld_up, a.in_type) &&
                    aligned(a.q, a.ld_q, 8);
   const bool wide = a.in_type == TS_DT_FP32;

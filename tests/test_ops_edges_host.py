@@ -74,3 +74,13 @@ def test_pointers_off_their_elements_are_refused(B, op, over):  # noqa: F811
     """A load there would fault the GPU."""
     args = dict(rmsnorm=norm_args, act_quant=act_args, fp8_matmul=matmul_args, balance=balance_args)[op](B, **over)
     refused(B, getattr(B.lib, "ts_moe_" + op), args, "aligned to its elements")
+
+
+@pytest.mark.parametrize("rows,cols,qs_row,qs_group", [(2, 300, 0, 1), (2, 300, 3, 0), (1, 129, 5, 0), (5, 100, 0, 1), (4, 300, 1, 1),
+                                                       (4, 300, 1, 3), (4, 300, 4, 2), (3, 300, -2, 1), (2, 200, 0, 0)])
+def test_scales_that_would_overlap_are_refused(B, rows, cols, qs_row, qs_group):  # noqa: F811
+    places = [r * qs_row + g * qs_group for r in range(rows) for g in range(-(-cols // 128))]
+    assert len(set(places)) < len(places)
+    wide = dict(rows=rows, qs_row=qs_row, qs_group=qs_group, ld_q=cols)
+    refused(B, B.lib.ts_moe_rmsnorm, norm_args(B, hidden=cols, ld_resid=cols, ld_delta=cols, ld_resid_out=cols, ld_y=cols, **wide), "q_scale overlap")
+    refused(B, B.lib.ts_moe_act_quant, act_args(B, inter=cols, ld_gate=cols, ld_up=cols, **wide), "q_scale overlap")
