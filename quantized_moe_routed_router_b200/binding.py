@@ -316,6 +316,11 @@ def _scales(t: torch.Tensor, what: str, shape: tuple, dev: int) -> tuple:
     return t.stride()
 
 
+# The current stream's handle.  torch.cuda.current_stream(dev).cuda_stream builds an object for it, which takes 2 us; the
+# direct call is torch's own but not public, so it may be missing.
+_current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+
+
 class _Op:
     """An entry point whose argument struct is packed in one go: building the ctypes struct costs a decode step's call
     about a microsecond more."""
@@ -331,7 +336,7 @@ class _Op:
         if dev < 0:
             _refuse("the tensors must be on a CUDA device")
         if stream is None:
-            stream = torch._C._cuda_getCurrentRawStream(dev)  # torch.cuda.current_stream(dev).cuda_stream takes 2 us
+            stream = _current_stream(dev)
         elif isinstance(stream, torch.cuda.Stream):
             if stream.device.index != dev:
                 _refuse(f"the stream belongs to {stream.device}, the tensors to {_name(dev)}")

@@ -245,3 +245,25 @@ def test_balance_gradient_against_differences_over_many_ctas(B, score, M, E, K):
         room = 0.5 * f * h * h / 6 * 4 * 6 * (2 * u.abs().max()) ** 3 + abs(up) * 2.0 ** -50 / h
         assert abs(got - want) <= float((tol * u.abs()).sum() + room), (got, want, float(room))
         assert abs(want) > 20 * float(room)      # the differences say something
+
+
+# ----------------------------------------------------------------------------- the binding's stream
+
+def test_current_stream_without_torchs_private_name(B, monkeypatch):
+    """The binding loads and runs on the current stream where torch lacks the direct call."""
+    import importlib.util
+    monkeypatch.delattr(torch._C, "_cuda_getCurrentRawStream")
+    spec = importlib.util.spec_from_file_location("quantized_moe_routed_router_b200.binding_again", B.__file__)
+    again = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(again)
+    x, y = gen(1)(5, 256), torch.empty(5, 256, device="cuda")
+    for s in (torch.cuda.current_stream(), torch.cuda.Stream()):
+        with torch.cuda.stream(s):
+            assert again._current_stream(0) == s.cuda_stream
+            again.rmsnorm(x, None, 1e-5, y=y)
+        torch.cuda.synchronize()
+        want = torch.empty_like(y)
+        B.rmsnorm(x, None, 1e-5, y=want)
+        assert torch.equal(y, want)
+        y.zero_()
+        torch.cuda.synchronize()
