@@ -179,10 +179,6 @@ MatmulPlan matmul_plan(const ts_moe_fp8_matmul_args& a, int sms) {
   const int row_ctas = cdiv(a.n, RW_N);
   if (!a.offsets && a.rows <= RW_MAX_ROWS && row_ctas <= 2 * sms && kb <= (a.rows <= 8 ? 32 : 16))
     return {MatmulPlan::ROWS, 0, 1, row_ctas};
-  // Groups: the sizes are not known here.  Up to 16 rows a group on average the narrow tiles read the matrices faster
-  // (32 groups of 5760 x 2880: 64 rows 72.6 against 79.4, 256 rows 85.5 against 94.0); beyond, groups take more tiles than
-  // one (1024 rows 114 against 103; 64 groups of 2816 x 2048, 2048 rows 84 against 71).
-  if (G > 1 && mean > 16) return tile;
   const int bt = mean <= 16 ? 16 : 32;
   const int64_t items = (cdiv(a.rows, bt) + reached - 1) * cdiv(a.n, ST_N);
   // K is split while that leaves one CTA an SM, or two where one would leave K whole, never into a second wave: a cluster
@@ -191,8 +187,12 @@ MatmulPlan matmul_plan(const ts_moe_fp8_matmul_args& a, int sms) {
   const int splits = (int)std::max<int64_t>(1, std::min<int64_t>(std::min(MAX_SPLITS, kb), (items * 2 <= sms ? sms : 2 * sms) / items));
   // A split makes at most sms or 2 sms CTAs of all items: every cluster has one item, as the kernel's join needs it.
   const MatmulPlan stream = {MatmulPlan::STREAM, bt, splits, (int)std::min<int64_t>(items, 2 * sms / splits)};
-  if (G > 1) return stream;
-  // One matrix: what each would take, by 0.5 a block of K and tile against a fixed 5 and the larger of 0.13 a block in
+  // Groups: the sizes are not known here.  Up to 32 rows a group on average the narrow tiles read the matrices faster
+  // (stream : tile; 32 groups of 5760 x 2880: 64 rows 72.6 : 79.4, 640 rows 90 : 105, 1024 rows 100 : 109, 1536 rows 116 : 116,
+  // 2048 rows 137 : 120; 64 groups of 2816 x 2048: 1280 rows 67 : 75, 3072 rows 82 : 77).
+  if (G > 1 && mean <= 32) return stream;
+  // One matrix, or larger groups (then with the most tiles that there can be; 4 groups of 256 x 1024 x 2048 in all 13.8 : 8.4,
+  // 2 of 100 x 512 x 4096 21.0 : 7.2, 8 of 1024 x 1408 x 2048 15.3 : 17.0): what each would take, by 0.5 a block of K and tile against a fixed 5 and the larger of 0.13 a block in
   // sequence and the traffic from L2 at 8 TB/s (tile : stream: 128 x 2880 x 2880 16.1 : 9.8, 333 x 2048 x 1408 10.7 : 7.6,
   // 600 x 1024 x 1024 9.2 : 6.4, 256 x 4096 x 1024 9.2 : 9.2, 128 x 14336 x 4096 22.7 : 36.7).  Tiles wait for what they
   // add, and shift rows at odd places.

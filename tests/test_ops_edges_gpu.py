@@ -5,7 +5,7 @@ import pytest
 import torch
 
 from tests import ops_ref as R
-from tests.test_ops_gpu import BF16, FP16, FP32, gen, routed, run_balance
+from tests.test_ops_gpu import BF16, FP16, FP32, gen, grouped, routed, run_balance
 
 pytestmark = pytest.mark.gpu
 
@@ -128,6 +128,15 @@ def test_fp8_matmul_wait_that_runs_out_in_a_group(B):
     assert len(lost) == 1, lost
     B.fp8_matmul(a, sa, b, sb, out, offsets=offsets)
     assert torch.equal(out, want)
+
+
+@pytest.mark.parametrize("sizes,N,K,tail", [
+    ([20] * 32, 300, 260, 1), ([1, 60, 0, 33, 32, 31, 65, 0], 520, 512, 3), ([25] * 8, 512, 1408, 0), ([90, 10], 391, 1300, 2),
+    ([0, 255, 0, 1], 1024, 520, 5)])
+def test_fp8_matmul_groups_of_medium_size(B, sizes, N, K, tail):
+    """Groups that end inside a tile of 32 rows, K whole and shared."""
+    for t, add in ((BF16, False), (FP32, True)):
+        grouped(B, sizes, N, K, t, tail=tail, add=add)
 
 
 # ----------------------------------------------------------------------------- far below the sigmoid's own range

@@ -84,3 +84,14 @@ def test_scales_that_would_overlap_are_refused(B, rows, cols, qs_row, qs_group):
     wide = dict(rows=rows, qs_row=qs_row, qs_group=qs_group, ld_q=cols)
     refused(B, B.lib.ts_moe_rmsnorm, norm_args(B, hidden=cols, ld_resid=cols, ld_delta=cols, ld_resid_out=cols, ld_y=cols, **wide), "q_scale overlap")
     refused(B, B.lib.ts_moe_act_quant, act_args(B, inter=cols, ld_gate=cols, ld_up=cols, **wide), "q_scale overlap")
+
+
+# the kernels' times for these groups lie 8 to 190 % apart: stream where K can be shared or tiles would mostly be empty
+@pytest.mark.parametrize("G,M,N,K,kind", [
+    (32, 64, 5760, 2880, 1), (32, 640, 5760, 2880, 1), (64, 1280, 2816, 2048, 1), (8, 200, 512, 4096, 1), (2, 100, 512, 4096, 1),
+    (4, 256, 1024, 2048, 1), (8, 1024, 1408, 2048, 2), (32, 3072, 5760, 2880, 2), (64, 24576, 2816, 2048, 2), (4, 400, 14336, 4096, 2)])
+def test_grouped_products_take_the_faster_kernel(B, G, M, N, K, kind):  # noqa: F811
+    a = matmul_args(B, rows=M, n=N, k=K, num_groups=G, ld_out=N, add=None)
+    plan = (C.c_int32 * 4)()
+    B.lib.ts_moe_debug_fp8_matmul_plan(C.byref(a), 148, plan)
+    assert plan[0] == kind, list(plan)
