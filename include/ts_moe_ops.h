@@ -53,7 +53,8 @@ enum { TS_DT_BF16 = 0, TS_DT_FP16 = 1, TS_DT_FP32 = 2 };
  *   v = r / sqrt(mean(r^2) + eps) * gamma        (float32 throughout)
  * resid_out <- r, y <- v rounded to y_type, q / q_scale <- v as 8-bit rows.
  * The norm reads the rounded r, so a fused call equals an addition stored to
- * the stream followed by a norm of the stream. */
+ * the stream followed by a norm of the stream.  A row whose sum of squares
+ * passes float32's largest value (|r| near 2^64 / sqrt(hidden)) gives v = 0. */
 typedef struct {
   int32_t rows;        /* 0 .. TS_MOE_MAX_ROWS */
   int32_t hidden;      /* 1 .. 16384 */
@@ -105,7 +106,8 @@ ts_moe_status ts_moe_act_quant(const ts_moe_act_quant_args* args, void* stream);
 
 /* Product of 8-bit rows with an 8-bit matrix whose scales cover 128 x 128 blocks:
  *   out[m][n] = sum_c a_scale[m][c] * b_scale[n / 128][c] * sum_{k in block c} a[m][k] * b[n][k]  (+ add[m][n])
- * with float32 sums, rounded once to out_type.  Grouped form (offsets given):
+ * with float32 sums, rounded once to out_type.  The two scales' product is formed
+ * first, in float32: it should stay in the normal range.  Grouped form (offsets given):
  * b is [num_groups][n][k], and rows offsets[g] .. offsets[g + 1] - 1 use matrix
  * g; the other rows of out are left as they were.  offsets is device memory and
  * is read on the device: the host neither knows nor waits for the group sizes.

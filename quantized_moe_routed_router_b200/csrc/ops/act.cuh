@@ -68,8 +68,9 @@ TSM_DEV bool any_far(const Raw<WIDE> (&g)[2], uint32_t far) {
 
 // A warp takes four neighbouring groups of a row, eight lanes and two chunks of eight columns a lane each; quads
 // row-major.  step_rows, step_quads: the grid's warps as whole rows of quads and the rest, so that the loop divides
-// nothing.  With VEC the next quad's loads are issued before this one is worked on: 8192 x 14336 bf16 in 96 us
-// (6.1 TB/s, HBM bounds it); without, and with 16 lanes a group and IEEE divisions, 162 us.
+// nothing.  With VEC the next quad's loads are issued before this one is worked on: 8192 x 14336 bf16 in 95 us
+// (6.2 TB/s, HBM bounds it), clamped in 104 us; without, and with 16 lanes a group and IEEE divisions, 162 us.  The far
+// gates' way as a branch beside the other cost 6 us; chosen before the conversions, and with values in pairs, none.
 template <bool VEC, bool WIDE, bool CLAMPED>
 __global__ void __launch_bounds__(ACT_THREADS, VEC && WIDE ? 2 : 4)
     act_quant_kernel(const ts_moe_act_quant_args a, int quads, int step_rows, int step_quads, uint32_t far) {

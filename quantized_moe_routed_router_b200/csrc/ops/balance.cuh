@@ -21,7 +21,7 @@ constexpr int BAL_ALONE = 256;  // threads of the only CTA of a small call
 constexpr int BAL_THREADS = 1024;  // otherwise: 32 warps a SM to hide the loads
 constexpr int BAL_WARPS = BAL_THREADS / 32;
 constexpr int BAL_MAX_E = TS_MOE_MAX_EXPERTS;
-constexpr int BAL_MAX_CTAS = 148;  // one per SM: part of the workspace's size, so fixed
+constexpr int BAL_MAX_CTAS = GPU_SMS;  // part of the workspace's size, so fixed
 constexpr int BAL_COUNT_CTAS = 128, BAL_COUNT_THREADS = 512, BAL_COUNT_LD = BAL_MAX_E + 4;
 static_assert(BAL_COUNT_CTAS <= BAL_ALONE, "one thread per counting CTA");
 static_assert(BAL_MAX_E <= BAL_ALONE, "one thread per expert in the finish");

@@ -9,6 +9,7 @@
 
 namespace tsm {
 
+constexpr int GPU_SMS = 148;  // a B200's; kernels that walk over rows size their grids by it, so another number costs time only
 constexpr int SCALE_BLOCK = TS_MOE_SCALE_BLOCK;
 constexpr float E4M3_MAX = 448.f;
 constexpr float AMAX_FLOOR = 0x1p-100f;  // the smallest amax a scale is formed from: scale and 1 / scale stay normal
@@ -244,12 +245,11 @@ TSM_DEV uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
 // columns: chunk c of lane l stands at column (c LANES + l) 8 of the group (lanes
 // past the row's end hold zeros).  Writes the group's E4M3 codes and, from its
 // first lane, its scale.  Both are rounded quotients: with 16-bit inputs some
-// values in a thousand stand exactly between two codes, and a product with an
+// values in ten thousand stand exactly between two codes, and a product with an
 // approximate reciprocal put a tenth of those on the other one.  A group's values
 // share the reciprocal, so a quotient costs two FMAs more than a product, and two
-// values share an instruction.  The
-// conversion saturates, so the group's largest value lands on 448 whichever way
-// it rounds.
+// values share an instruction: 16384 x 4096 norm 98.5 -> 100.7 us.  The conversion
+// saturates, so the group's largest value lands on 448 whichever way it rounds.
 template <int LANES, bool VEC>
 TSM_DEV void quant_group(const float (&v)[16 / LANES][8], uint8_t* q, int64_t off, int n, float* scale) {
   constexpr int C = 16 / LANES;

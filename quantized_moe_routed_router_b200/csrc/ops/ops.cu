@@ -214,11 +214,13 @@ cudaError_t launch_norm_rows(const ts_moe_rmsnorm_args& a, void* stream) {
   int per_sm = 1;
   const cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, k, threads, 0);
   if (e != cudaSuccess) return e;
-  return launch(k, dim3(std::min(a.rows, 148 * std::max(per_sm, 1))), threads, 0, stream, a);
+  return launch(k, dim3(std::min(a.rows, GPU_SMS * std::max(per_sm, 1))), threads, 0, stream, a);
 }
 
 cudaError_t launch_norm(const ts_moe_rmsnorm_args& a, bool vec, void* stream) {
   const int chunks = cdiv(a.hidden, 8);
+  // Many rows (us, a CTA a row : CTAs that walk, bf16: 512 x 512 2.5 : 2.9, 512 x 5120 6.8 : 7.1, 1024 x 2048 5.1 : 5.6,
+  // 1024 x 4096 12.5 : 9.7, 2048 x 2880 16.1 : 13.7, 2048 x 4096 21.9 : 16.4, 4096 x 8192 89 : 63; fp32: 1024 x 5120 15.5 : 17.0)
   if (vec && a.rows > 1024)
     return a.hidden <= 4096   ? launch_norm_rows<256>(a, stream)
            : a.hidden <= 8192 ? launch_norm_rows<512>(a, stream)
@@ -314,7 +316,7 @@ ts_moe_status ts_moe_act_quant(const ts_moe_act_quant_args* args, void* stream) 
   const int quads = cdiv(a.inter, 4 * SCALE_BLOCK);
   const int64_t units = (int64_t)a.rows * quads;
   const int resident = vec && wide ? 2 : 4;  // CTAs per SM by the kernel's launch bounds
-  const int grid = (int)std::min<int64_t>((units + ACT_THREADS / 32 - 1) / (ACT_THREADS / 32), 148 * resident);
+  const int grid = (int)std::min<int64_t>((units + ACT_THREADS / 32 - 1) / (ACT_THREADS / 32), GPU_SMS * resident);
   const int warps = grid * (ACT_THREADS / 32);
   auto k = a.act == TS_ACT_SWIGLU ? act_instance<false>(vec, wide) : act_instance<true>(vec, wide);
   return done(launch(k, dim3(grid), ACT_THREADS, 0, stream, a, quads, warps / quads, warps % quads, act_far_bits(a)), "act_quant launch");
@@ -393,6 +395,8 @@ ts_moe_status ts_moe_debug_fp8_matmul_held(const ts_moe_fp8_matmul_args* args, i
   return fp8_matmul(args, cta, wait_us, stream);
 }
 
+// Up to 16384 logits one CTA does everything: the counting launch and the joins take longer than it (us, one CTA : many, with
+// the gradient: 512 x 32 6.8 : 7.9, 64 x 256 6.5 : 8.5, 1024 x 32 9.9 : 8.2, 256 x 256 13.4 : 9.7).
 static int balance_ctas(int rows, int experts) {
   if ((int64_t)rows * experts <= 16384) return 1;
   return std::min(cdiv(rows, BAL_WARPS * (32 / balance_lanes(experts))), BAL_MAX_CTAS);
@@ -438,6 +442,8 @@ ts_moe_status ts_moe_balance(const ts_moe_balance_args* args, void* stream) {
   const bool sigmoid = a.score == TS_SCORE_SIGMOID_RENORM, wide = a.dtype == TS_DT_FP32;
   auto k = sigmoid ? (wide ? balance_instance<true, true>(a.experts) : balance_instance<true, false>(a.experts))
                    : (wide ? balance_instance<false, true>(a.experts) : balance_instance<false, false>(a.experts));
+  // fewer warps meet at fewer barriers (us, 256 threads : 1024: 64 x 32 3.7 : 4.1, 16 x 256 4.1 : 4.9, 128 x 32 4.6 : 4.4,
+  // 256 x 32 6.3 : 5.4, 64 x 256 7.5 : 6.5)
   const int threads = (int64_t)a.rows * a.experts <= 4096 ? BAL_ALONE : BAL_THREADS;
   return done(launch(k, dim3(ctas), threads, 0, stream, p), "balance launch");
 }

@@ -38,7 +38,7 @@ def same_codes(q, s, v):
 
 @pytest.mark.parametrize("M,H", [(2000, 4096), (1100, 8192), (40, 16384), (300, 1001)])
 def test_norm_codes_are_the_quotients(B, M, H):
-    """From the kernel's own float32 rows: 16-bit inputs put some values in a thousand exactly between two codes, where an
+    """From the kernel's own float32 rows: 16-bit inputs put some values in ten thousand exactly between two codes, where an
     approximate quotient takes the wrong one."""
     r = gen(M)
     resid, gamma = (r(M, H) * torch.exp(r(M, 1))).to(BF16), (1 + 0.2 * r(H)).to(BF16)
