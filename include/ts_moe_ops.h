@@ -23,9 +23,11 @@
  *   - 8-bit rows are E4M3 (finite range +-448, 0x7F = NaN) with one float32
  *     scale per 128 consecutive columns of a row, the last group of a row being
  *     short where the width is no multiple of 128; an element is q * scale.
- *     They are formed as scale = max(amax, 2^-100) / 448, q = e4m3(v / scale)
- *     (round to nearest even): a group of zeros has a normal scale, and a NaN or
- *     an infinity in a group makes its scale, and so its values, non-finite.
+ *     They are formed as scale = max(amax, 2^-100) * (1 / 448), the reciprocal and
+ *     the product rounded to float32, and q = e4m3(v / scale), the quotient by that
+ *     scale rounded to float32 and then to nearest even: a group of zeros has a
+ *     normal scale, and a NaN or an infinity in a group makes its scale, and so
+ *     its values, non-finite.
  *   - Every function returns a ts_moe_status; on failure
  *     ts_moe_last_error(NULL) gives the reason on the calling thread.  A call
  *     with no rows returns TS_MOE_OK and does nothing, except that

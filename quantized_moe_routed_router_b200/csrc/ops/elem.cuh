@@ -207,13 +207,6 @@ TSM_DEV float min_nan(float a, float b) {
   return r;
 }
 
-// a / b rounded, from r, the rounded 1 / b: one FMA forms what the first quotient leaves of a, exactly while nothing in it
-// is subnormal, and another adds its share (Markstein, IBM Journal of Research and Development 34, 1990).
-TSM_DEV float quotient(float a, float b, float r) {
-  const float q = a * r;
-  return fmaf(fmaf(-q, b, a), r, q);
-}
-
 // Two values to an instruction.
 TSM_DEV uint64_t pair(float x, float y) {
   uint64_t r;
@@ -244,12 +237,16 @@ TSM_DEV uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
 // LANES neighbouring lanes hold the 128 columns of one group in chunks of eight
 // columns: chunk c of lane l stands at column (c LANES + l) 8 of the group (lanes
 // past the row's end hold zeros).  Writes the group's E4M3 codes and, from its
-// first lane, its scale.  Both are rounded quotients: with 16-bit inputs some
-// values in ten thousand stand exactly between two codes, and a product with an
-// approximate reciprocal put a tenth of those on the other one.  A group's values
-// share the reciprocal, so a quotient costs two FMAs more than a product, and two
-// values share an instruction: 16384 x 4096 norm 98.5 -> 100.7 us.  The conversion
-// saturates, so the group's largest value lands on 448 whichever way it rounds.
+// first lane, its scale, amax times the rounded 1 / 448.  The codes are of the
+// rounded quotients by that scale: with 16-bit inputs some values in ten thousand
+// stand exactly between two codes, and a product with an approximate reciprocal put
+// a tenth of those on the other one.  One FMA forms what a first quotient q0 = v r
+// (r the rounded 1 / scale) leaves of v, exactly while nothing in it is subnormal,
+// and another adds its share (Markstein, IBM Journal of Research and Development 34,
+// 1990).  A group's values share r, so a quotient costs two FMAs more than a
+// product, and two values share an instruction: 16384 x 4096 norm 98.7 -> 99.9 us.
+// The conversion saturates, so the group's largest value lands on 448 whichever way
+// it rounds.
 template <int LANES, bool VEC>
 TSM_DEV void quant_group(const float (&v)[16 / LANES][8], uint8_t* q, int64_t off, int n, float* scale) {
   constexpr int C = 16 / LANES;
@@ -261,7 +258,7 @@ TSM_DEV void quant_group(const float (&v)[16 / LANES][8], uint8_t* q, int64_t of
   }
 #pragma unroll
   for (int d = LANES / 2; d >= 1; d >>= 1) m = max_nan(m, __shfl_xor_sync(0xFFFFFFFFu, m, d, LANES));
-  const float s = m <= FLT_MAX ? quotient(m, E4M3_MAX, 1.f / E4M3_MAX) : m;
+  const float s = m * (1.f / E4M3_MAX);
   // A tiny group is taken times 2^64, which keeps the remainders out of the subnormal range; for an infinite scale they are
   // left out (0 and NaN stay what they are).  The reciprocal is rounded by the same step from the approximate one.
   const bool tiny = s < 0x1p-60f;
@@ -285,7 +282,7 @@ TSM_DEV void quant_group(const float (&v)[16 / LANES][8], uint8_t* q, int64_t of
   for (int c = 0; c < C; ++c) {
     uint32_t h[4];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {  // quotient(), two values at a time
+    for (int j = 0; j < 4; ++j) {
       const uint64_t q0 = mul2(t[c][j], inv2);
       h[j] = __nv_cvt_float2_to_fp8x2(unpair(fma2(fma2(q0, rest2, t[c][j]), inv2, q0)), __NV_SATFINITE, __NV_E4M3);
     }

@@ -21,11 +21,11 @@ def B():
 # ----------------------------------------------------------------------------- codes are rounded quotients
 
 def codes(v):
-    """(codes, scales) of float32 v from the definition: scale = max(amax, 2^-100) / 448, code = e4m3(v / scale), each
-    quotient rounded to float32."""
+    """(codes, scales) of float32 v from the definition: scale = max(amax, 2^-100) * (1 / 448), code = e4m3(v / scale), the
+    reciprocal, the product and the quotient each rounded to float32."""
     M, K = v.shape
     p = torch.nn.functional.pad(v.cpu(), (0, R.blocks(K) * 128 - K)).view(M, -1, 128)
-    s = p.abs().amax(-1).clamp_min(2.0 ** -100) / 448.0
+    s = p.abs().amax(-1).clamp_min(2.0 ** -100) * torch.tensor(1.0 / 448.0)
     return (p / s[..., None]).view(M, -1)[:, :K].to(torch.float8_e4m3fn), s
 
 
