@@ -382,7 +382,7 @@ static ts_moe_status fp8_matmul(const ts_moe_fp8_matmul_args* args, int held, un
 ts_moe_status ts_moe_fp8_matmul(const ts_moe_fp8_matmul_args* args, void* stream) { return fp8_matmul(args, -1, 0, stream); }
 
 void ts_moe_debug_fp8_matmul_plan(const ts_moe_fp8_matmul_args* args, int sms, int32_t plan[4]) {
-  const MatmulPlan p = matmul_plan(*args, sms);
+  const MatmulPlan p = args->rows > 0 ? matmul_plan(*args, sms) : MatmulPlan{MatmulPlan::ROWS, 0, 1, 0};  // no rows: no launch
   plan[0] = p.kind;
   plan[1] = p.bt;
   plan[2] = p.splits;

@@ -43,6 +43,8 @@ def test_a_split_product_has_a_cluster_for_every_item(B):  # noqa: F811
         assert splits <= min(4, -(-K // 128)) and grid * splits <= 2 * sms
         assert splits == 1 or grid >= items, (M, N, K, G, sms, list(plan))
     assert {(0, 1), (1, 1), (1, 2), (1, 4), (2, 1)} <= seen
+    B.lib.ts_moe_debug_fp8_matmul_plan(C.byref(matmul_args(B, rows=0)), 148, plan)
+    assert plan[3] == 0
 
 
 def test_binding_refuses_tensors_of_other_dimensions(B):  # noqa: F811
