@@ -149,7 +149,7 @@ TSM_DEV void balance_quad(const uint32_t (&q)[WIDE ? 4 : 2], int type, float (&v
 
 // SIGMOID: the score.  WIDE: logits and their gradient in 32 bits.
 // 65536 x 256 sigmoid with the gradient: 45 us with the counting launch (134 MB, floor 20.8); issue slots bound the pass
-// over the logits (69 % busy, some 40 instructions a logit).
+// over the logits (71 % busy, 38 instructions a logit counted); that instance spills 32 bytes at 64 registers.
 template <int LPR, int NV, bool SIGMOID, bool WIDE>
 __global__ void __launch_bounds__(BAL_THREADS) balance_kernel(const BalanceParams p) {
   constexpr int N = 4 * NV;

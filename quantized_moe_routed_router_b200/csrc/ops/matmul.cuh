@@ -346,7 +346,8 @@ TSM_DEV void store_tile(const MatmulParams& p, const CUtensorMap* mo, float (&ac
 // Persistent, a tile at a time; the MMAs of a tile's first blocks run while the last one is stored.  Per block of K the
 // MMAs of 128 x 256 take 512 cycles at the tensor pipe's peak, and so does nothing else alone; what bounds the kernel is
 // the chain from the MMAs' end over the read-back to the next MMAs in the same half of tensor memory, and the chip's
-// power: 8192 x 14336 x 4096 in 476 us (2.0 PFLOP/s, tensor pipe 52 %), 312 us with the sums taken out.  128 rows, not
+// power: 8192 x 14336 x 4096 in 480 us at first (2.0 PFLOP/s, tensor pipe 53 %), 550 us over a second, when the clock has come
+// down to 1.5 GHz (1.75 PFLOP/s); 312 us with the sums taken out.  The adders' 128 sums each spill 160 bytes.  128 rows, not
 // 256: groups waste half a tile on average.
 __global__ void __launch_bounds__(TL_THREADS, 1)
     fp8_tile_kernel(const __grid_constant__ MatmulParams p, const __grid_constant__ CUtensorMap ma,
@@ -547,7 +548,7 @@ struct StreamSmem {
 };
 
 // The matrix as the MMA's first operand: 128 of its rows are one instruction's, whatever few tokens there are.  64 routes
-// over 32 experts of 5760 x 2880 in 75.8 us (6.1 TB/s: HBM bounds it); 16 x 5760 x 2880 in 6.7 us, of which 2.6 us are
+// that reach 28 of 32 experts of 5760 x 2880 in 76.2 us (6.1 TB/s: HBM bounds it); 16 x 5760 x 2880 in 6.3 us, of which 2.6 us are
 // traffic and the rest a chain of latencies (launch, TMA, MMA, read-back, the cluster's sum).
 template <int BT>
 __global__ void __launch_bounds__(ST_THREADS, StreamShape<BT>::CTAS)
