@@ -280,9 +280,13 @@ def _rows(t: torch.Tensor, what: str, rows: int, cols: int, dev: int) -> int:
     return ld if rows > 1 else max(ld, cols)
 
 
-def _dims(t: torch.Tensor, what: str, dims: str):
-    if t.dim() != dims.count(",") + 1:
+def _dims(t: torch.Tensor, what: str, dims: str) -> tuple:
+    """The sizes of a tensor of two dimensions."""
+    try:
+        rows, cols = t.shape
+    except ValueError:
         _refuse(f"{what} must be [{dims}], not {list(t.shape)}")
+    return rows, cols
 
 
 def _name(dev: int) -> str:
@@ -366,8 +370,7 @@ def rmsnorm(resid: torch.Tensor, gamma: Optional[torch.Tensor], eps: float, delt
     """ts_moe_rmsnorm: r = resid + delta (kept in resid_out, which may be resid),
     v = r / sqrt(mean(r^2) + eps) * gamma, written to y [M, H] and/or as 8-bit
     rows to q [M, H] with q_scale [M, ceil(H / 128)] (any strides)."""
-    _dims(resid, "resid", "M, H")
-    M, H = resid.shape
+    M, H = _dims(resid, "resid", "M, H")
     dev = resid.get_device()
     rt = _type(resid, "resid")
     ld = _rows(resid, "resid", M, H, dev)
@@ -397,8 +400,7 @@ def act_quant(gate: torch.Tensor, up: torch.Tensor, act: int, q: torch.Tensor, q
               act_alpha: float = 1.702, act_limit: float = 7.0, stream=None):
     """ts_moe_act_quant: the activation of gate and up ([M, I], e.g. two halves
     of one product) as 8-bit rows q [M, I] with q_scale [M, ceil(I / 128)]."""
-    _dims(gate, "gate", "M, I")
-    M, inter = gate.shape
+    M, inter = _dims(gate, "gate", "M, I")
     dev = gate.get_device()
     if up.dtype != gate.dtype:
         _refuse("gate and up must have one type")
@@ -420,10 +422,8 @@ def fp8_matmul(a: torch.Tensor, a_scale: torch.Tensor, b: torch.Tensor, b_scale:
     is allowed).  b is [N, K], or with offsets (int32 [G + 1] on the device)
     [G, N, K] with b_scale [G, ..., ...]: rows offsets[g] .. offsets[g + 1] - 1
     use b[g], other rows of out are left as they were."""
-    _dims(a, "a", "M, K")
-    _dims(out, "out", "M, N")
-    M, K = a.shape
-    N = out.shape[1]
+    M, K = _dims(a, "a", "M, K")
+    N = _dims(out, "out", "M, N")[1]
     dev = a.get_device()
     kb = -(-K // 128)
     _codes(a, "a")
@@ -459,11 +459,9 @@ def balance(logits: torch.Tensor, idx: torch.Tensor, score: int, loss: torch.Ten
     balance loss (float32, one element) and, with dlogits [M, E], its gradient
     times dloss (float32, one element; None = 1).  mask: bool or uint8 [M], rows
     that count.  Without a workspace one is taken from torch's allocator."""
-    _dims(logits, "logits", "M, E")
-    _dims(idx, "idx", "M, K")
-    M, E = logits.shape
+    M, E = _dims(logits, "logits", "M, E")
+    K = _dims(idx, "idx", "M, K")[1]
     dev = logits.get_device()
-    K = idx.shape[1]
     if idx.dtype != torch.int32:
         _refuse(f"idx is {idx.dtype}; int32 is needed")
     pm = pd = pp = po = pg = ldg = 0
