@@ -189,7 +189,7 @@ MatmulPlan matmul_plan(const ts_moe_fp8_matmul_args& a, int sms) {
   const MatmulPlan stream = {MatmulPlan::STREAM, bt, splits, (int)std::min<int64_t>(items, 2 * sms / splits)};
   // Groups: the sizes are not known here.  Up to 32 rows a group on average the narrow tiles read the matrices faster
   // (stream : tile; 32 groups of 5760 x 2880: 64 rows 72.6 : 79.4, 640 rows 90 : 105, 1024 rows 100 : 109, 1536 rows 116 : 116,
-  // 2048 rows 137 : 120; 64 groups of 2816 x 2048: 1280 rows 67 : 75, 3072 rows 82 : 77).
+  // 2048 rows 137 : 120; 64 groups of 2816 x 2048: 1280 rows 67 : 75, 4096 rows 94 : 85).
   if (G > 1 && mean <= 32) return stream;
   // One matrix, or larger groups (then with the most tiles that there can be; 4 groups of 256 x 1024 x 2048 in all 13.8 : 8.4,
   // 2 of 100 x 512 x 4096 21.0 : 7.2, 8 of 1024 x 1408 x 2048 15.3 : 17.0): what each would take, by 0.5 a block of K and tile against a fixed 5 and the larger of 0.13 a block in
