@@ -188,14 +188,14 @@ MatmulPlan matmul_plan(const ts_moe_fp8_matmul_args& a, int sms) {
   // A split makes at most sms or 2 sms CTAs of all items: every cluster has one item, as the kernel's join needs it.
   const MatmulPlan stream = {MatmulPlan::STREAM, bt, splits, (int)std::min<int64_t>(items, 2 * sms / splits)};
   // Groups: the sizes are not known here.  Up to 32 rows a group on average the narrow tiles read the matrices faster
-  // (stream : tile; 32 groups of 5760 x 2880: 64 rows 72.6 : 79.4, 640 rows 90 : 105, 1024 rows 100 : 109, 1536 rows 116 : 116,
-  // 2048 rows 137 : 120; 64 groups of 2816 x 2048: 1280 rows 67 : 75, 4096 rows 94 : 85).
+  // (tile : stream; 32 groups of 5760 x 2880: 64 rows 79.4 : 72.6, 640 rows 105 : 90, 1024 rows 109 : 100, 1536 rows 116 : 116,
+  // 2048 rows 120 : 137; 64 groups of 2816 x 2048: 1280 rows 75 : 67, 4096 rows 85 : 94).
   if (G > 1 && mean <= 32) return stream;
-  // One matrix, or larger groups (then with the most tiles that there can be; 4 groups of 256 x 1024 x 2048 in all 13.8 : 8.4,
-  // 2 of 100 x 512 x 4096 21.0 : 7.2, 8 of 1024 x 1408 x 2048 15.3 : 17.0): what each would take, by 0.5 a block of K and tile against a fixed 5 and the larger of 0.13 a block in
-  // sequence and the traffic from L2 at 8 TB/s (tile : stream: 128 x 2880 x 2880 16.1 : 9.8, 333 x 2048 x 1408 10.7 : 7.6,
-  // 600 x 1024 x 1024 9.2 : 6.4, 256 x 4096 x 1024 9.2 : 9.2, 128 x 14336 x 4096 22.7 : 36.7).  Tiles wait for what they
-  // add, and shift rows at odd places.
+  // One matrix, or larger groups with the most tiles that they can make: what each would take, by 0.5 a block of K and tile
+  // against a fixed 5 and the larger of 0.13 a block in sequence and the traffic from L2 at 8 TB/s (tile : stream:
+  // 128 x 2880 x 2880 16.1 : 9.8, 333 x 2048 x 1408 10.7 : 7.6, 600 x 1024 x 1024 9.2 : 6.4, 256 x 4096 x 1024 9.2 : 9.2,
+  // 128 x 14336 x 4096 22.7 : 36.7; groups, rows of all: 2 of 512 x 4096, 100 rows 21.0 : 7.2, 4 of 1024 x 2048, 256 rows
+  // 13.8 : 8.4, 8 of 1408 x 2048, 1024 rows 15.3 : 17.0).  Tiles wait for what they add, and shift rows at odd places.
   const double rest = (a.add ? 5.0 : 0.0) + (aligned(a.out, a.ld_out * dt_size(a.out_type), 16) ? 0.0 : 3.0);
   const double t_tile = 4.0 + (double)((tiles + sms - 1) / sms) * (1.5 + 0.5 * kb + rest);
   const double t_stream = 5.0 + std::max(0.13 * (double)((items * splits + 2 * sms - 1) / (2 * sms)) * cdiv(kb, splits),
