@@ -570,12 +570,14 @@ __global__ void __launch_bounds__(ST_THREADS, StreamShape<BT>::CTAS)
     prefetch_map(&ma);
     prefetch_map(&mb);
   }
+  cluster_sync();  // the peers' barriers are ready
+  // Tensor memory is taken after the cluster has met: from here on a CTA that holds some waits for its peers for a limited
+  // time only.  Before, a peer that waits for tensor memory (which has no limit) could have kept it from others for good.
   if (warp == 1) tmem_alloc<S::COLS>(&s.tmem);
   if (warp == 0 && !p.a.offsets) fill_groups(p.a, BT, s.groups);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  cluster_sync();  // the peers' barriers are ready
   // what needs no other kernel's results comes before the wait for them: divisions here took most of a microsecond
   const uint32_t tmem = s.tmem;
   const int nt = cdiv(p.a.n, ST_N);
